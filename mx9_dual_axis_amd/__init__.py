@@ -21,6 +21,11 @@ plus the signatures the pages use: ``mxfp8_quantize_2d_1x32_32x1`` (dense
 when ``offs`` is None, grouped otherwise), ``convert_to_mx9`` and
 ``convert_from_mx9`` (with an axis), and their single-tensor forms
 ``convert_to_mx9_packed`` / ``convert_from_mx9_packed``.
+
+``routed`` holds what stands between the tokens of a routed-expert layer and
+these calls (routing with its balance loss, dispatch, combine, their
+gradients) and the product of 8-bit integer codes; its names are the package's
+too.
 """
 from __future__ import annotations
 
@@ -685,3 +690,7 @@ def convert_to_mx9_packed(x: torch.Tensor, block_size: int = 16, axis: int = -1)
 def convert_from_mx9_packed(packed, out_dtype, shape, block_size: int = 16, axis: int = -1):
     """Inverse of convert_to_mx9_packed; the shape and axis are not stored."""
     return mx9_unpack_records(packed, shape, axis, out_dtype, block_size)
+
+
+from .routed import (MXRouting, i8_gemm_nt, i8_grouped_gemm_rows, i8_linear, i8_quantize_rows,  # noqa: E402,F401
+                     mx_combine, mx_combine_grad, mx_dispatch, mx_dispatch_i8, mx_route, mx_route_grad, mx_routing)

@@ -10,46 +10,13 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "mxq_host.h"
 #include "mxq_kernels.h"
 
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 constexpr int64_t kMaxDual = int64_t(1) << 24;   // dual-axis: 32-bit per-lane offsets within a tile
-constexpr uint64_t kMaxThreads = 0xFFFFFFFFull - 256;   // grid.x * block.x must fit 32 bits
-
-struct Span {
-    uintptr_t p;
-    uint64_t n;   // bytes
-};
-
-bool overlap(const Span& a, const Span& b) {
-    return a.n != 0 && b.n != 0 && a.p < b.p + b.n && b.p < a.p + a.n;
-}
-
-bool any_overlap(const Span* s, int k) {
-    for (int i = 0; i < k; ++i)
-        for (int j = i + 1; j < k; ++j)
-            if (overlap(s[i], s[j])) return true;
-    return false;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
-
-// No device buffer spans more bytes than a 48-bit virtual address space.
-constexpr uint64_t kMaxSpan = uint64_t(1) << 48;
-constexpr uint64_t kTooLarge = ~uint64_t(0);
-
-// Bytes spanned by a [rows, cols] matrix with row pitch ld (elements), or
-// kTooLarge when that exceeds kMaxSpan (computed without overflow).
-uint64_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esz) {
-    if (rows <= 0 || cols <= 0) return 0;
-    const unsigned __int128 b =
-        (static_cast<unsigned __int128>(rows - 1) * uint64_t(ld) + uint64_t(cols)) * uint64_t(esz);
-    return b > kMaxSpan ? kTooLarge : uint64_t(b);
-}
 
 int check_dual(const uint16_t* x, int64_t M, int64_t N, int64_t ld_x, int32_t block_size,
                int32_t scaling_mode, const uint8_t* q_row, const uint8_t* s_row,

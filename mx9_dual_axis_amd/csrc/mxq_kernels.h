@@ -71,4 +71,43 @@ hipError_t launch_scales_to_mfma(const uint8_t* s, int64_t rs, int64_t bs, int64
 hipError_t launch_scales_from_mfma(const uint8_t* in, int64_t rows, int64_t blocks, uint8_t* s, int64_t rs, int64_t bs,
                                    hipStream_t stream);
 
+// Expert routing of T tokens over E <= 1024 experts, k <= 16 picks each, and
+// the gradient of its weights and balance loss (route.hip).  M is at least
+// T k + min(E, T k) (align - 1).  workspace: route_workspace bytes, 4-byte
+// aligned.  dweight and dloss may be null.
+int64_t route_workspace(int64_t T, int32_t E);
+hipError_t launch_route(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld, const uint8_t* valid,
+                        int32_t k, bool normalize, int32_t align, int64_t M, int32_t* idx, float* weight,
+                        int32_t* slot, int32_t* src, int32_t* counts, int32_t* offs, int32_t* live, float* prob,
+                        float* loss, void* workspace, hipStream_t stream);
+hipError_t launch_route_grad(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld, const uint8_t* valid,
+                             int32_t k, bool normalize, const int32_t* idx, const float* weight, const float* dweight,
+                             const int32_t* counts, const int32_t* live, const float* dloss, void* dlogits,
+                             int64_t ld_d, hipStream_t stream);
+
+// Token rows to and from their experts' rows (routed_rows.hip); pitches in
+// elements, N, K > 0.  launch_quantize_rows with slot == nullptr sends row t
+// to row t (M = T).  combine and combine_grad: weight null means 1; dweight
+// may be null.  The *_blocks functions give the grids.
+uint64_t dispatch_blocks(int64_t T, int64_t M, int64_t row_bytes);
+uint64_t combine_blocks(int64_t T, int64_t row_bytes);
+uint64_t token_blocks(int64_t T, int64_t M);
+hipError_t launch_dispatch(const void* x, int dtype, int64_t T, int64_t N, int64_t ld_x, const int32_t* slot,
+                           const int32_t* src, int32_t k, int64_t M, void* out, int64_t ld_out, hipStream_t stream);
+hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t K, int64_t ld_x, const int32_t* slot,
+                                const int32_t* src, int32_t k, int64_t M, int8_t* q, int64_t ld_q, float* s,
+                                hipStream_t stream);
+hipError_t launch_combine(const void* rows, int dtype, int64_t M, int64_t N, int64_t ld_r, const int32_t* slot,
+                          const float* weight, int32_t k, int64_t T, void* y, int64_t ld_y, hipStream_t stream);
+hipError_t launch_combine_grad(const void* dy, int dtype, int64_t T, int64_t N, int64_t ld_dy, const void* rows,
+                               int64_t ld_r, const int32_t* slot, const float* weight, const int32_t* src, int32_t k,
+                               int64_t M, void* drows, int64_t ld_d, float* dweight, hipStream_t stream);
+
+// Product of 8-bit codes, C = A B^T with row scales (i8_gemm.hip); offs null:
+// dense.  M, N > 0, K <= 131071.
+uint64_t i8_gemm_blocks(int64_t M, int64_t N, bool groups, int32_t G);
+hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
+                          const float* sB, int64_t sb_gs, const float* bias, void* C, int64_t ldc, int64_t M,
+                          int64_t N, int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);
+
 }  // namespace mxq

@@ -1,0 +1,393 @@
+"""Binding of ``include/mxq_routed.h``: routing, dispatch, 8-bit integer
+products and combine of a routed-expert layer.
+
+  mx_routing(T, E, k, align)              -> an MXRouting, the outputs and workspace of mx_route
+  mx_route(logits, k, valid)              -> MXRouting (idx, weight, slot, src, counts, offs, live, prob, loss)
+  mx_route_grad(logits, routing, dweight, dloss, valid) -> dlogits
+  mx_dispatch(x, slot, src)               -> rows of the padded buffer
+  mx_dispatch_i8(x, slot, src)            -> (q, s), the same rows as int8 codes and scales
+  i8_quantize_rows(x)                     -> (q, s)
+  i8_gemm_nt(A, sA, B, sB, bias)          -> C = A B^T
+  i8_linear(x, B, sB, bias)               -> the product of x, quantized on the way
+  i8_grouped_gemm_rows(A, sA, B, sB, offs) -> C, each group's rows with its expert's B[g]
+  mx_combine(rows, slot, weight)          -> y, the weighted sum of each token's expert rows
+  mx_combine_grad(dy, rows, slot, weight, src) -> (drows, dweight)
+
+As in the package's other calls, every step runs in the library's kernels on
+the current stream, outputs are allocated with torch unless `out` is given,
+and a refused call raises before anything is launched.
+"""
+from __future__ import annotations
+
+import torch
+
+_ESZ = {torch.float32: 0, torch.bfloat16: 1}      # MX_DTYPE_F32, MX_DTYPE_BF16
+_I32, _I8, _F32 = torch.int32, torch.int8, torch.float32
+
+
+def _argtypes(lib):
+    import ctypes
+
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    lib.mx_route_rows.argtypes = [I64, I32, I32, I32]
+    lib.mx_route_workspace.argtypes = [I64, I32]
+    lib.i8_linear_workspace.argtypes = [I64, I64]
+    for f in (lib.mx_route_rows, lib.mx_route_workspace, lib.i8_linear_workspace):
+        f.restype = I64
+    lib.mx_route.argtypes = [P, I32, I64, I32, I64, P, I32, I32, I32, I64, P, P, P, P, P, P, P, P, P, P, I64, P]
+    lib.mx_route_grad.argtypes = [P, I32, I64, I32, I64, P, I32, I32, P, P, P, P, P, P, P, I64, P]
+    lib.mx_dispatch.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, I64, P]
+    lib.mx_dispatch_i8.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, I64, P, P]
+    lib.i8_quantize_rows.argtypes = [P, I32, I64, I64, I64, P, I64, P, P]
+    lib.i8_gemm_nt.argtypes = [P, I64, P, P, I64, P, P, I64, I64, I64, P, I64, I32, P]
+    lib.i8_linear.argtypes = [P, I32, I64, P, I64, P, P, I64, I64, I64, P, I64, I32, P, I64, P]
+    lib.i8_grouped_gemm_rows.argtypes = [P, I64, P, P, I64, I64, P, I64, P, I32, I64, I64, I64, P, I64, I32, P]
+    lib.mx_combine.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, I64, P]
+    lib.mx_combine_grad.argtypes = [P, I32, I64, I64, I64, P, I64, P, P, P, I32, I64, P, I64, P, P]
+    for f in (lib.mx_route, lib.mx_route_grad, lib.mx_dispatch, lib.mx_dispatch_i8, lib.i8_quantize_rows,
+              lib.i8_gemm_nt, lib.i8_linear, lib.i8_grouped_gemm_rows, lib.mx_combine, lib.mx_combine_grad):
+        f.restype = ctypes.c_int
+
+
+_lib = None
+
+
+def _L():
+    global _lib
+    if _lib is None:
+        from . import library
+
+        lib = library()
+        _argtypes(lib)
+        _lib = lib
+    return _lib
+
+
+def _run(dev, f, *args):
+    """Call an entry point on `dev`'s current stream and raise on a status."""
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc:
+        from . import MXError, status_string
+
+        raise MXError(rc, status_string(rc))
+
+
+def _matrix(t, name, dtypes, dev=None):
+    """A 2-d device tensor with contiguous rows; returns its row pitch."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {tuple(t.shape)}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+    rows, cols = t.shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return max(pitch, cols)
+    if pitch < cols:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return pitch
+
+
+def _flat(t, name, dtype, shape, dev):
+    """A contiguous device tensor of one dtype and shape; returns its pointer."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _valid(valid, T, dev):
+    if valid is None:
+        return None
+    if valid.dtype is torch.bool:
+        return _flat(valid, "valid", torch.bool, (T,), dev)
+    return _flat(valid, "valid", torch.uint8, (T,), dev)
+
+
+def _out_matrix(out, name, shape, dtype, dev):
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        return out, shape[1]
+    pitch = _matrix(out, name, (dtype,), dev)
+    if out.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(out.shape)}")
+    return out, pitch
+
+
+class MXRouting:
+    """Outputs and workspace of mx_route for one (T, E, k, align), reused from
+    call to call; made by mx_routing.
+
+    idx, weight, slot [T, k]; src [rows]; counts, offs, prob [E]; live, loss
+    [1]: see mx_route.  `normalize` is what the last mx_route used."""
+
+    __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "idx", "weight", "slot", "src", "counts",
+                 "offs", "live", "prob", "loss", "_workspace", "_ptrs")
+
+    def __init__(self, T, E, k, align, device):
+        lib = _L()
+        self.T, self.E, self.k, self.align = int(T), int(E), int(k), int(align)
+        self.rows = lib.mx_route_rows(self.T, self.E, self.k, self.align)
+        if self.rows < 0:
+            raise ValueError(f"no routing of T={T}, E={E}, k={k}, align={align}: T >= 0, 1 <= E <= 1024, "
+                             "1 <= k <= min(E, 16), 1 <= align <= 65536 and T k <= 2^30 are needed")
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("device must be a GPU")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.normalize = dev, True
+        e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+        self.idx, self.weight, self.slot = e((T, k), _I32), e((T, k), _F32), e((T, k), _I32)
+        self.src, self.counts, self.offs = e((self.rows,), _I32), e((E,), _I32), e((E,), _I32)
+        self.live, self.prob, self.loss = e((1,), _I32), e((E,), _F32), e((1,), _F32)
+        size = lib.mx_route_workspace(self.T, self.E)
+        self._workspace = e((size,), torch.uint8)
+        self._ptrs = tuple(t.data_ptr() for t in (self.idx, self.weight, self.slot, self.src, self.counts, self.offs,
+                                                  self.live, self.prob, self.loss, self._workspace)) + (size,)
+
+
+def mx_routing(T: int, E: int, k: int, align: int = 128, device="cuda") -> MXRouting:
+    """The buffers of mx_route for T tokens, E experts and k picks each, groups
+    padded to multiples of `align` (128 for the MXFP8 grouped calls)."""
+    return MXRouting(T, E, k, align, device)
+
+
+def mx_route(logits: torch.Tensor, k: int | None = None, valid: torch.Tensor | None = None, normalize: bool = True,
+             align: int = 128, out: MXRouting | None = None) -> MXRouting:
+    """Softmax routing of logits [T, E] (float32 or bfloat16, rows at any
+    pitch) to the k best experts of each token.
+
+    valid (bool or uint8 [T]) leaves tokens out, a logit of -inf an expert.
+    The result's weight are the picks' probabilities, over their sum when
+    `normalize`; counts, offs, slot and src describe the padded buffer that
+    the grouped casts and products take; loss is the balance loss."""
+    ld = _matrix(logits, "logits", _ESZ)
+    T, E = logits.shape
+    dev = logits.device
+    if out is None:
+        if k is None:
+            raise ValueError("k is needed when out is not given")
+        out = MXRouting(T, E, k, align, dev)
+    elif out.T != T or out.E != E or out.device != dev or (k is not None and k != out.k):
+        raise ValueError(f"out was made for T={out.T}, E={out.E}, k={out.k} on {out.device}, the call has T={T}, "
+                         f"E={E}, k={k} on {dev}")
+    p = out._ptrs
+    _run(dev, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, dev), out.k,
+         1 if normalize else 0, out.align, out.rows, *p)
+    out.normalize = bool(normalize)
+    return out
+
+
+def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tensor | None = None,
+                  dloss: torch.Tensor | None = None, valid: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the routing's weight (dweight float32 [T, k]) and loss
+    (dloss float32 [1]) with respect to the logits, in their dtype."""
+    ld = _matrix(logits, "logits", _ESZ)
+    T, E = logits.shape
+    dev = logits.device
+    if routing.T != T or routing.E != E or routing.device != dev:
+        raise ValueError("routing was made for other logits")
+    dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), dev)
+    dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), dev)
+    out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, dev)
+    p = routing._ptrs
+    _run(dev, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, dev), routing.k,
+         1 if routing.normalize else 0, p[0], p[1], dw, p[4], p[6], dl, out.data_ptr(), ld_d)
+    return out
+
+
+def _slots(slot, dev):
+    if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
+        raise ValueError("slot must be an int32 [T, k] tensor")
+    T, k = slot.shape
+    return _flat(slot, "slot", _I32, (T, k), dev), T, k
+
+
+def _src(src, dev):
+    if not isinstance(src, torch.Tensor) or src.dim() != 1:
+        raise ValueError("src must be an int32 [M] tensor")
+    M = src.shape[0]
+    return _flat(src, "src", _I32, (M,), dev), M
+
+
+def mx_dispatch(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out: torch.Tensor | None = None):
+    """Rows of the padded buffer: x[t] at slot[t, j] for every pick, 0 where
+    src is -1.  x is float32 or bfloat16 [T, N] with rows at any pitch."""
+    ld = _matrix(x, "x", _ESZ)
+    dev = x.device
+    sp, T, k = _slots(slot, dev)
+    rp, M = _src(src, dev)
+    if T != x.shape[0]:
+        raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
+    N = x.shape[1]
+    out, ld_o = _out_matrix(out, "out", (M, N), x.dtype, dev)
+    _run(dev, _L().mx_dispatch, x.data_ptr(), _ESZ[x.dtype], T, N, ld, sp, rp, k, M, out.data_ptr(), ld_o)
+    return out
+
+
+def _codes_out(out, rows, K, dev):
+    """(q, its pitch, s): new codes get rows of whole 16-byte pieces, which the
+    products read fastest."""
+    if out is None:
+        pitch = (K + 15) // 16 * 16
+        q = torch.empty((rows, pitch), dtype=_I8, device=dev)
+        return (q if pitch == K else q[:, :K]), pitch, torch.empty((rows,), dtype=_F32, device=dev)
+    q, s = out
+    q, pitch = _out_matrix(q, "out[0]", (rows, K), _I8, dev)
+    _flat(s, "out[1]", _F32, (rows,), dev)
+    return q, pitch, s
+
+
+def mx_dispatch_i8(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out=None):
+    """mx_dispatch with each row quantized: (q int8 [M, K], s float32 [M])."""
+    ld = _matrix(x, "x", _ESZ)
+    dev = x.device
+    sp, T, k = _slots(slot, dev)
+    rp, M = _src(src, dev)
+    if T != x.shape[0]:
+        raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
+    K = x.shape[1]
+    q, pitch, s = _codes_out(out, M, K, dev)
+    _run(dev, _L().mx_dispatch_i8, x.data_ptr(), _ESZ[x.dtype], T, K, ld, sp, rp, k, M, q.data_ptr(), pitch,
+         s.data_ptr())
+    return q, s
+
+
+def i8_quantize_rows(x: torch.Tensor, out=None):
+    """(q int8 [T, K], s float32 [T]): x[t] ~ q[t] s[t], s = max |x[t]| / 127."""
+    ld = _matrix(x, "x", _ESZ)
+    T, K = x.shape
+    q, pitch, s = _codes_out(out, T, K, x.device)
+    _run(x.device, _L().i8_quantize_rows, x.data_ptr(), _ESZ[x.dtype], T, K, ld, q.data_ptr(), pitch, s.data_ptr())
+    return q, s
+
+
+def _bias(bias, N, dev):
+    return None if bias is None else _flat(bias, "bias", _F32, (N,), dev)
+
+
+def _product_out(out, shape, out_dtype, dev):
+    if out is None:
+        if out_dtype not in _ESZ:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
+        return torch.empty(shape, dtype=out_dtype, device=dev), shape[1]
+    if out.dtype not in _ESZ:
+        raise ValueError(f"out must be float32 or bfloat16, not {out.dtype}")
+    return _out_matrix(out, "out", shape, out.dtype, dev)
+
+
+def i8_gemm_nt(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
+               bias: torch.Tensor | None = None, out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
+    """C = A B^T: int8 codes A [M, K] and B [N, K] (rows at any pitch), float32
+    scales sA [M] and sB [N], optional float32 bias [N]."""
+    lda = _matrix(A, "A", (_I8,))
+    dev = A.device
+    ldb = _matrix(B, "B", (_I8,), dev)
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("A and B must share the contraction extent")
+    sa, sb, bi = _flat(sA, "sA", _F32, (M,), dev), _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
+    out, ldc = _product_out(out, (M, N), out_dtype, dev)
+    _run(dev, _L().i8_gemm_nt, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
+         _ESZ[out.dtype])
+    return out
+
+
+def i8_linear(x: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, bias: torch.Tensor | None = None, out_dtype=None,
+              out: torch.Tensor | None = None):
+    """i8_quantize_rows of x [M, K] and i8_gemm_nt in one call; the result has
+    x's dtype unless out_dtype or out says otherwise."""
+    ld = _matrix(x, "x", _ESZ)
+    dev = x.device
+    ldb = _matrix(B, "B", (_I8,), dev)
+    M, K = x.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise ValueError("x and B must share the contraction extent")
+    sb, bi = _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
+    out, ldc = _product_out(out, (M, N), out_dtype or x.dtype, dev)
+    size = M * ((K + 15) // 16 * 16) + (M * 4 + 15) // 16 * 16
+    ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+    _run(dev, _L().i8_linear, x.data_ptr(), _ESZ[x.dtype], ld, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
+         _ESZ[out.dtype], ws.data_ptr(), size)
+    return out
+
+
+def i8_grouped_gemm_rows(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, offs: torch.Tensor,
+                         out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
+    """Rows of group g (cumulative int32 ends offs [G], groups of any size) with
+    expert g's codes B[g] ([E, N, K], E >= G) and scales sB[g] ([E, N]); rows
+    from offs[-1] on give 0."""
+    lda = _matrix(A, "A", (_I8,))
+    dev = A.device
+    M, K = A.shape
+    if not isinstance(B, torch.Tensor) or B.dtype is not _I8 or B.dim() != 3 or B.device != dev:
+        raise ValueError("B must be int8 [E, N, K] codes on the device of A")
+    E, N = B.shape[0], B.shape[1]
+    if B.shape[2] != K or (K > 1 and B.stride(2) != 1) or (N > 1 and B.stride(1) < K):
+        raise ValueError("B must be [E, N, K] codes with contiguous rows that share A's contraction extent")
+    if not isinstance(sB, torch.Tensor) or sB.dtype is not _F32 or sB.shape != (E, N) or sB.device != dev or (
+            N > 1 and sB.stride(1) != 1):
+        raise ValueError("sB must be a float32 [E, N] tensor with contiguous rows")
+    if not isinstance(offs, torch.Tensor) or offs.dim() != 1 or not 1 <= offs.shape[0] <= E:
+        raise ValueError("offs must be an int32 [G] tensor with 1 <= G <= E")
+    G = offs.shape[0]
+    sa, of = _flat(sA, "sA", _F32, (M,), dev), _flat(offs, "offs", _I32, (G,), dev)
+    out, ldc = _product_out(out, (M, N), out_dtype, dev)
+    _run(dev, _L().i8_grouped_gemm_rows, A.data_ptr(), lda, sa, B.data_ptr(), max(B.stride(1), K), B.stride(0),
+         sB.data_ptr(), sB.stride(0), of, G, M, N, K, out.data_ptr(), ldc, _ESZ[out.dtype])
+    return out
+
+
+def mx_combine(rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor | None = None,
+               out: torch.Tensor | None = None):
+    """y[t] = sum_j weight[t, j] rows[slot[t, j]] (weight None: 1) over the
+    picks that have a slot."""
+    ld = _matrix(rows, "rows", _ESZ)
+    dev = rows.device
+    sp, T, k = _slots(slot, dev)
+    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
+    M, N = rows.shape
+    out, ld_y = _out_matrix(out, "out", (T, N), rows.dtype, dev)
+    _run(dev, _L().mx_combine, rows.data_ptr(), _ESZ[rows.dtype], M, N, ld, sp, wp, k, T, out.data_ptr(), ld_y)
+    return out
+
+
+def mx_combine_grad(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor | None,
+                    src: torch.Tensor, out=None):
+    """(drows, dweight) of mx_combine for dy [T, N]: drows[slot[t, j]] =
+    weight[t, j] dy[t], 0 where src is -1; dweight[t, j] = <dy[t],
+    rows[slot[t, j]]>."""
+    ld_g = _matrix(dy, "dy", _ESZ)
+    dev = dy.device
+    ld_r = _matrix(rows, "rows", (dy.dtype,), dev)
+    sp, T, k = _slots(slot, dev)
+    rp, M = _src(src, dev)
+    N = dy.shape[1]
+    if dy.shape[0] != T or rows.shape != (M, N):
+        raise ValueError(f"dy must be [{T}, N] and rows [{M}, N], not {tuple(dy.shape)} and {tuple(rows.shape)}")
+    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
+    drows, dweight = out if out is not None else (None, None)
+    drows, ld_d = _out_matrix(drows, "out[0]", (M, N), dy.dtype, dev)
+    if dweight is None:
+        dweight = torch.empty((T, k), dtype=_F32, device=dev)
+    dp = _flat(dweight, "out[1]", _F32, (T, k), dev)
+    _run(dev, _L().mx_combine_grad, dy.data_ptr(), _ESZ[dy.dtype], T, N, ld_g, rows.data_ptr(), ld_r, sp, wp, rp, k, M,
+         drows.data_ptr(), ld_d, dp)
+    return drows, dweight
