@@ -444,6 +444,298 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
     }
 }
 
+// ---- many tiles, aligned operands: pipelined through LDS ----
+//
+// WM x WN waves, each (16 MS) x (16 NS) of the tile.  A stage holds 128 codes
+// of every row of both operands; buffer loads put 16-byte pieces from memory
+// straight into LDS (no registers stage them), the swizzle applied to the
+// address they read, and run kStages - 1 steps ahead.  Loads complete in
+// order, so a step waits only until the later steps' loads are the ones
+// outstanding; wait and barrier are one asm block, because the compiler's
+// barrier would wait for every load.  Within a step a wave keeps all its A
+// fragments and reads B one column ahead of the instructions.
+//
+// Rows past the tile's last repeat it.  In the last step, pieces past the
+// end of the contraction (K is whole pieces) load that step's first piece
+// again; A's are then cleared in LDS, and any integer times 0 is 0.
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ v4i pipe_rsrc(const int8_t* base, uint64_t bytes) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    return v4i{uniform(int32_t(uint32_t(b))), uniform(int32_t(uint32_t(b >> 32))), uniform(int32_t(uint32_t(bytes))),
+               0x00020000};
+}
+// 16 bytes per lane from voff + soff of the buffer to LDS at lds + 16 lane.
+__device__ __forceinline__ void pipe_load16(v4i r, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds)
+                 : "memory");
+}
+// The same, hinting that the line is not read again from this L2.
+__device__ __forceinline__ void pipe_load16_nt(v4i r, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voff), "s"(r), "s"(soff), "{m0}"(lds)
+                 : "memory");
+}
+// At most kLeft loads of this wave outstanding, its LDS accesses done, then
+// the workgroup's barrier.
+template <int kLeft>
+__device__ __forceinline__ void pipe_sync() {
+    static_assert(kLeft >= 0 && kLeft < 64, "vmcnt immediate");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+
+template <int MS, int NS, int WM, int WN>
+struct Pipe {
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int kTM = 16 * MS * WM, kTN = 16 * NS * WN;
+    static constexpr int kLA = kTM / 8 / kWaves, kLB = kTN / 8 / kWaves;    // loads per wave and step
+    static constexpr uint32_t kB = uint32_t(kTM) * 128, kStage = kB + uint32_t(kTN) * 128;
+    static constexpr int kStages = (152 * 1024) / kStage >= 3 ? 3 : 2;
+    static constexpr uint32_t kScales = kStages * kStage;                   // sA, sB, bias of the tile
+    static constexpr uint32_t kLds = kScales + uint32_t(kTM + 2 * kTN) * 4;
+    static constexpr int kLoads = kLA + kLB;
+    static_assert(kLA * kWaves * 8 == kTM && kLB * kWaves * 8 == kTN && kLds <= 160 * 1024, "tile");
+    static_assert(kThreads >= kTM && kThreads >= kTN, "scales: one per thread");
+};
+
+__device__ __forceinline__ v8i fragment(const v4i* tile, uint32_t row, uint32_t lane) {
+    const uint32_t g = lane >> 4, sw = lane & 7u;                           // row % 8 == lane % 8
+    const v4i lo = tile[row * 8u + (g ^ sw)], hi = tile[row * 8u + ((4u + g) ^ sw)];
+    return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+}
+__device__ __forceinline__ v4i lo4(const v8i& v) { return v4i{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ v4i hi4(const v8i& v) { return v4i{v[4], v[5], v[6], v[7]}; }
+
+// Row tiles of the groups, and all of them with the tail's.
+template <int TM>
+__device__ void count_tiles(const int32_t* offs, int32_t G, int64_t M, uint32_t* covered, uint32_t* all) {
+    const uint32_t lane = threadIdx.x & 63u;
+    int32_t end_carry = 0;
+    uint32_t tiles = 0;
+    for (int32_t base = 0; base < G; base += 64) {
+        const int32_t g = base + int32_t(lane);
+        int32_t c = g < G ? offs[g] : 0;
+        c = c < 0 ? 0 : (int64_t(c) > M ? int32_t(M) : c);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(c, d, 64);
+            if (lane >= uint32_t(d)) c = max(c, o);
+        }
+        c = max(c, end_carry);
+        int32_t start = __shfl_up(c, 1, 64);
+        if (lane == 0) start = end_carry;
+        uint32_t own = uint32_t(c - start + TM - 1) / uint32_t(TM);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) own += uint32_t(__shfl_xor(int(own), d, 64));
+        tiles += uint32_t(uniform(int32_t(own)));
+        end_carry = uniform(__shfl(c, 63, 64));
+    }
+    *covered = tiles;
+    *all = tiles + uint32_t((M - end_carry + TM - 1) / TM);
+}
+
+template <typename O, int MS, int NS, int WM, int WN, bool kStreamB>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_kernel(I8Args p) {
+    using P = Pipe<MS, NS, WM, WN>;
+    constexpr int kEsz = int(sizeof(O));
+    constexpr int kPitch = 16 * NS * kEsz + 16;                             // staged result row, bytes
+    __shared__ __attribute__((aligned(16))) uint8_t lds[P::kLds];
+    static_assert(P::kWaves * 16 * kPitch <= int(P::kScales), "result staging");
+
+    const uint32_t t = threadIdx.x, lane = t & 63u;
+    const uint32_t wave = uint32_t(uniform(int32_t(t >> 6)));
+    const uint32_t wm = wave / WN, wn = wave % WN;
+
+    // Workgroups are dealt to the 8 XCDs in turn, each with its own L2.  Row
+    // groups: XCD x takes a contiguous eighth of the covered row tiles, all
+    // column tiles of a row tile in a row, then its eighth of the tail.
+    RowTile r;
+    uint32_t tn;
+    bool zero = false;
+    if (p.offs != nullptr) {
+        const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3, lr = j / p.tiles_n;
+        tn = j - lr * p.tiles_n;
+        uint32_t cov, all;
+        count_tiles<P::kTM>(p.offs, p.G, p.M, &cov, &all);
+        const uint32_t tail = all - cov;
+        const uint32_t c0 = uint32_t(uint64_t(cov) * xcd / 8u), c1 = uint32_t(uint64_t(cov) * (xcd + 1u) / 8u);
+        const uint32_t t0 = cov + uint32_t(uint64_t(tail) * xcd / 8u), t1 = cov + uint32_t(uint64_t(tail) * (xcd + 1u) / 8u);
+        uint32_t tm;
+        if (lr < c1 - c0) tm = c0 + lr;
+        else if (lr < (c1 - c0) + (t1 - t0)) tm = t0 + (lr - (c1 - c0));
+        else return;                                                        // uniform
+        if (!find_tile<P::kTM>(p.offs, p.G, p.M, tm, &r)) return;
+        zero = r.g >= p.G;
+    } else {
+        r.m0 = int64_t(blockIdx.x % p.tiles_m) * P::kTM;
+        r.m1 = p.M;
+        r.g = 0;
+        tn = blockIdx.x / p.tiles_m;
+    }
+    const int64_t n0 = int64_t(tn) * P::kTN;
+    const uint32_t rows = uint32_t(min(int64_t(P::kTM), r.m1 - r.m0)), cols = uint32_t(min(int64_t(P::kTN), p.N - n0));
+    const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs) + n0 * p.ldb;
+    const float* sB = p.sB + (zero ? 0 : int64_t(r.g) * p.sb_gs) + n0;
+    const uint32_t K = uint32_t(p.K), n = zero ? 0u : (K + 127u) / 128u;
+
+    // load plan: load j of an operand fills rows 8 j .. 8 j + 7 of its tile
+    const uint32_t lda = uint32_t(p.lda), ldb = uint32_t(p.ldb);
+    const uint32_t lr = lane >> 3, lc = 16u * ((lane & 7u) ^ lr);
+    const v4i ra = pipe_rsrc(p.A + r.m0 * p.lda, uint64_t(rows - 1u) * lda + K);
+    const v4i rb = pipe_rsrc(B, uint64_t(cols - 1u) * ldb + K);
+    uint32_t va[P::kLA], vb[P::kLB];
+#pragma unroll
+    for (int q = 0; q < P::kLA; ++q) va[q] = min(8u * (uint32_t(P::kLA) * wave + q) + lr, rows - 1u) * lda + lc;
+#pragma unroll
+    for (int q = 0; q < P::kLB; ++q) vb[q] = min(8u * (uint32_t(P::kLB) * wave + q) + lr, cols - 1u) * ldb + lc;
+    const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(lds));
+    const uint32_t cut = K % 128u != 0 && lc >= K % 128u ? lc : 0u;          // the last step's pieces past K read piece 0
+    auto issue = [&](uint32_t step, uint32_t stage) {
+        const uint32_t k = step * 128u, st = lds0 + stage * P::kStage, back = step + 1u == n ? cut : 0u;
+#pragma unroll
+        for (int q = 0; q < P::kLA; ++q) pipe_load16(ra, st + 1024u * (uint32_t(P::kLA) * wave + q), va[q] - back, k);
+#pragma unroll
+        for (int q = 0; q < P::kLB; ++q) {
+            const uint32_t at = st + P::kB + 1024u * (uint32_t(P::kLB) * wave + q);
+            if constexpr (kStreamB) pipe_load16_nt(rb, at, vb[q] - back, k);
+            else pipe_load16(rb, at, vb[q] - back, k);
+        }
+    };
+
+    v4i acc[MS][NS];
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+#pragma unroll
+    for (uint32_t s = 0; s + 1 < uint32_t(P::kStages); ++s)
+        if (s < n) issue(s, s);
+    {
+        // the tile's scales and bias, while the first stage is on its way
+        float* sc = reinterpret_cast<float*>(lds + P::kScales);
+        if (t < uint32_t(P::kTM)) sc[t] = p.sA[r.m0 + min(t, rows - 1u)];
+        if (t < uint32_t(P::kTN)) {
+            sc[P::kTM + t] = sB[min(t, cols - 1u)];
+            sc[P::kTM + P::kTN + t] = p.bias ? p.bias[n0 + min(t, cols - 1u)] : 0.f;
+        }
+    }
+    uint32_t stage = 0;
+    for (uint32_t s = 0; s < n; ++s) {
+        if constexpr (P::kStages == 3) {
+            if (s + 1 < n) pipe_sync<P::kLoads>();
+            else pipe_sync<0>();
+        } else {
+            pipe_sync<0>();
+        }
+        if (s + P::kStages - 1 < n) {
+            const uint32_t free = stage == 0 ? uint32_t(P::kStages - 1) : stage - 1u;
+            issue(s + P::kStages - 1, free);
+        }
+        uint8_t* st = lds + stage * P::kStage;
+        if (s + 1 == n && K % 128u != 0) {
+            const uint32_t c0 = K % 128u / 16u, left = 8u - c0;              // K is whole pieces
+            for (uint32_t c = t; c < left * uint32_t(P::kTM); c += uint32_t(P::kThreads)) {
+                const uint32_t row = c / left, piece = c0 + c % left;
+                reinterpret_cast<v4i*>(st)[row * 8u + (piece ^ (row & 7u))] = v4i{0, 0, 0, 0};
+            }
+            pipe_sync<0>();
+        }
+        const v4i* ta = reinterpret_cast<const v4i*>(st);
+        const v4i* tb = reinterpret_cast<const v4i*>(st + P::kB);
+        v8i a[MS];
+#pragma unroll
+        for (int i = 0; i < MS; ++i) a[i] = fragment(ta, wm * 16u * MS + 16u * i + (lane & 15u), lane);
+        v8i b = fragment(tb, wn * 16u * NS + (lane & 15u), lane);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            v8i nb = b;
+            if (j + 1 < NS) nb = fragment(tb, wn * 16u * NS + 16u * (j + 1) + (lane & 15u), lane);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo4(a[i]), lo4(b), acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi4(a[i]), hi4(b), acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            b = nb;
+        }
+        stage = stage + 1u == uint32_t(P::kStages) ? 0u : stage + 1u;
+    }
+    __syncthreads();
+
+    // ---- results through LDS, 16 rows of the wave tile at a time ----
+    const float* sc = reinterpret_cast<const float*>(lds + P::kScales);
+    uint8_t* ep = lds + wave * (16 * kPitch);
+    constexpr int kPieces = 16 * NS * kEsz / 16;                            // 16-byte pieces per staged row
+    O* C = static_cast<O*>(p.C);
+    const bool whole = reinterpret_cast<uintptr_t>(C) % 16 == 0 && (p.ldc * kEsz) % 16 == 0;
+    float sb[NS], bi[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        const uint32_t c = wn * 16u * NS + 16u * j + (lane & 15u);
+        sb[j] = sc[P::kTM + c];
+        bi[j] = sc[P::kTM + P::kTN + c];
+    }
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+        const uint32_t r0 = wm * 16u * MS + 16u * i;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const uint32_t row = 4u * (lane >> 4) + v;
+            const float sa = sc[r0 + row];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                float x = float(acc[i][j][v]) * sa;
+                x = p.bias ? __builtin_fmaf(x, sb[j], bi[j]) : x * sb[j];
+                reinterpret_cast<O*>(ep + row * kPitch)[16 * j + (lane & 15u)] = Out<O>::get(zero ? 0.f : x);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // lgkmcnt(0)
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 16 * kPieces / 64; ++q) {
+            const uint32_t piece = 64u * q + lane, row = piece / kPieces, pc = piece % kPieces;
+            const uint32_t col = wn * 16u * NS + pc * (16 / kEsz);
+            const uint8_t* from = ep + row * kPitch + 16u * pc;
+            if (r0 + row >= rows || col >= cols) continue;
+            O* to = C + (r.m0 + r0 + row) * p.ldc + n0 + col;
+            if (whole && col + 16 / kEsz <= cols) {
+                const uint4 val = *reinterpret_cast<const uint4*>(from);
+                const u32x4 vv = {val.x, val.y, val.z, val.w};
+                __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(to));
+            } else {
+                for (uint32_t e = 0; e < 16 / kEsz && col + e < cols; ++e) to[e] = reinterpret_cast<const O*>(from)[e];
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // reads done before the next rows' writes
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Workgroups of a pipelined product.
+template <int MS, int NS, int WM, int WN>
+uint64_t pipe_blocks(int64_t M, int64_t N, bool groups, int32_t G, int64_t* tiles_m, int64_t* tiles_n) {
+    using P = Pipe<MS, NS, WM, WN>;
+    *tiles_m = tile_bound(M, P::kTM, groups, G);
+    *tiles_n = (N + P::kTN - 1) / P::kTN;
+    // an XCD's share: at most a ceiling of the covered tiles and one of the tail's
+    return groups ? uint64_t(8 * ((*tiles_m + 7) / 8 + 1)) * uint64_t(*tiles_n) : uint64_t(*tiles_m) * uint64_t(*tiles_n);
+}
+
+template <typename O, int MS, int NS, int WM, int WN, bool kStreamB>
+hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
+    int64_t tm, tn;
+    const uint64_t blocks = pipe_blocks<MS, NS, WM, WN>(p.M, p.N, p.offs != nullptr, p.G, &tm, &tn);
+    p.tiles_m = uint32_t(tm);
+    p.tiles_n = uint32_t(tn);
+    hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, kStreamB>), dim3(uint32_t(blocks)), dim3(64 * WM * WN), 0,
+                       stream, p);
+    return hipGetLastError();
+}
+
 template <typename O, int MS, int NS, int kW, int kU, typename X>
 hipError_t launch_stream(I8Args& p, hipStream_t stream) {
     p.tiles_m = uint32_t(tile_bound(p.M, 16 * MS, p.offs != nullptr, p.G));
@@ -460,46 +752,66 @@ hipError_t launch_tiles(I8Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Which kernel: a streamed one of (16 MS) x (16 NS) tiles, or whole tiles.
+// Which kernel.
+enum class Kind { kStream, kTiles, kPipe };
 struct Form {
-    int ms, ns, threads;         // ms == 0: 128 x 128 tiles
+    Kind kind;
+    int ms, ns;                  // kStream: 16-row sub-tiles; kPipe: 0 = 256 x 256, 1 = 128 x 256
+    uint64_t threads;            // of the grid
 };
 
-Form choose(int64_t M, int64_t N, bool groups, int32_t G) {
+// pipe: the operands are whole aligned 16-byte pieces.
+Form choose(int64_t M, int64_t N, bool groups, int32_t G, bool pipe) {
+    auto stream = [&](int ms, int ns, int waves) {
+        return Form{Kind::kStream, ms, ns,
+                    uint64_t(tile_bound(M, 16 * ms, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 64u * uint64_t(waves)};
+    };
+    auto tiles = [&]() {
+        int64_t tm, tn;
+        if (pipe && groups) return Form{Kind::kPipe, 1, 0, pipe_blocks<4, 4, 2, 4>(M, N, groups, G, &tm, &tn) * 512};
+        if (pipe) return Form{Kind::kPipe, 0, 0, pipe_blocks<4, 8, 4, 2>(M, N, groups, G, &tm, &tn) * 512};
+        return Form{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
+    };
     if (groups) {
         const int64_t rows = (M + G - 1) / G;
-        if (rows <= 8) return {1, 2, 512};
-        if (rows <= 20) return {2, 2, 512};
-        if (rows <= 48) return {4, 2, 512};
-        return {0, 0, 256};
+        if (rows <= 8) return stream(1, 2, 8);
+        if (rows <= 20) return stream(2, 2, 8);
+        if (rows <= 48) return stream(4, 2, 8);
+        return tiles();
     }
-    if (M <= 16) return N >= 16384 ? Form{1, 2, 512} : Form{1, 1, 512};
-    const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    if (tiles >= 192) return {0, 0, 256};
-    return ((M + 63) / 64) * ((N + 63) / 64) >= 192 ? Form{4, 4, 256} : Form{2, 2, 512};
+    if (M <= 16) return N >= 16384 ? stream(1, 2, 8) : stream(1, 1, 8);
+    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return tiles();
+    return ((M + 63) / 64) * ((N + 63) / 64) >= 192 ? stream(4, 4, 4) : stream(2, 2, 8);
+}
+
+bool pipe_fits(const I8Args& p) {
+    const auto aligned = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+    return aligned(p.A) && aligned(p.B) && p.lda % 16 == 0 && p.ldb % 16 == 0 && p.b_gs % 16 == 0 && p.K % 16 == 0 &&
+           p.K > 0 && p.lda < (1 << 23) && p.ldb < (1 << 23);
 }
 
 template <typename O>
 hipError_t launch(I8Args& p, hipStream_t stream) {
-    const Form f = choose(p.M, p.N, p.offs != nullptr, p.G);
+    const Form f = choose(p.M, p.N, p.offs != nullptr, p.G, pipe_fits(p));
+    if (f.kind == Kind::kPipe)
+        return f.ms ? launch_pipe<O, 4, 4, 2, 4, true>(p, stream) : launch_pipe<O, 4, 8, 4, 2, false>(p, stream);
+    if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
     switch (f.ms * 8 + f.ns) {
         case 8 + 1: return launch_stream<O, 1, 1, 8, 8, void>(p, stream);
         case 8 + 2: return launch_stream<O, 1, 2, 8, 4, void>(p, stream);
         case 16 + 2: return launch_stream<O, 2, 2, 8, 4, void>(p, stream);
         case 32 + 2: return launch_stream<O, 4, 2, 8, 2, void>(p, stream);
-        case 32 + 4: return launch_stream<O, 4, 4, 4, 2, void>(p, stream);
-        default: return launch_tiles<O>(p, stream);
+        default: return launch_stream<O, 4, 4, 4, 2, void>(p, stream);
     }
 }
 
 }  // namespace
 
-// The threads of the grid that a product launches.
+// The threads of the largest grid that a product of this shape launches.
 uint64_t i8_gemm_threads(int64_t M, int64_t N, bool groups, int32_t G) {
     if (M <= 0 || N <= 0) return 0;
-    const Form f = choose(M, N, groups, G);
-    const int64_t tm = f.ms ? 16 * f.ms : kTile, tn = f.ms ? 16 * f.ns : kTile;
-    return uint64_t(tile_bound(M, tm, groups, G)) * uint64_t((N + tn - 1) / tn) * uint64_t(f.threads);
+    const uint64_t a = choose(M, N, groups, G, false).threads, b = choose(M, N, groups, G, true).threads;
+    return a > b ? a : b;
 }
 
 hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
