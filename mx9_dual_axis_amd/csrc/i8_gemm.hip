@@ -534,44 +534,125 @@ __device__ void count_tiles(const int32_t* offs, int32_t G, int64_t M, uint32_t*
     *all = tiles + uint32_t((M - end_carry + TM - 1) / TM);
 }
 
+// The tile of this workgroup.  Workgroups are dealt to the 8 XCDs in turn, each
+// with its own L2.  Row groups: XCD x takes a contiguous eighth of the covered
+// row tiles, all column tiles of a row tile in a row, then its eighth of the
+// tail.
+template <int TM>
+__device__ bool place_tile(const I8Args& p, RowTile* r, uint32_t* tn) {
+    if (p.offs == nullptr) {
+        r->m0 = int64_t(blockIdx.x % p.tiles_m) * TM;
+        r->m1 = p.M;
+        r->g = 0;
+        *tn = blockIdx.x / p.tiles_m;
+        return true;
+    }
+    const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3, lr = j / p.tiles_n;
+    *tn = j - lr * p.tiles_n;
+    uint32_t cov, all;
+    count_tiles<TM>(p.offs, p.G, p.M, &cov, &all);
+    const uint32_t tail = all - cov;
+    const uint32_t c0 = uint32_t(uint64_t(cov) * xcd / 8u), c1 = uint32_t(uint64_t(cov) * (xcd + 1u) / 8u);
+    const uint32_t t0 = cov + uint32_t(uint64_t(tail) * xcd / 8u), t1 = cov + uint32_t(uint64_t(tail) * (xcd + 1u) / 8u);
+    uint32_t tm;
+    if (lr < c1 - c0) tm = c0 + lr;
+    else if (lr < (c1 - c0) + (t1 - t0)) tm = t0 + (lr - (c1 - c0));
+    else return false;
+    return find_tile<TM>(p.offs, p.G, p.M, tm, r);
+}
+
+// The tile's scales and bias into LDS.
+template <typename P>
+__device__ __forceinline__ void load_scales(const I8Args& p, uint8_t* lds, const float* sB, const RowTile& r, int64_t n0,
+                                            uint32_t rows, uint32_t cols) {
+    const uint32_t t = threadIdx.x;
+    float* sc = reinterpret_cast<float*>(lds + P::kScales);
+    if (t < uint32_t(P::kTM)) sc[t] = p.sA[r.m0 + min(t, rows - 1u)];
+    if (t < uint32_t(P::kTN)) {
+        sc[P::kTM + t] = sB[min(t, cols - 1u)];
+        sc[P::kTM + P::kTN + t] = p.bias ? p.bias[n0 + min(t, cols - 1u)] : 0.f;
+    }
+}
+
+// A wave's staged rows (kCols columns at a pitch in bytes) to C: 16-byte
+// non-temporal stores where C allows them.
+template <typename O, int kCols, int kRows>
+__device__ __forceinline__ void store_rows(const I8Args& p, const uint8_t* ep, int pitch, int64_t row0, int64_t col0,
+                                           uint32_t rows, uint32_t cols) {
+    constexpr int kPer = 16 / int(sizeof(O)), kPieces = kCols / kPer;
+    const uint32_t lane = threadIdx.x & 63u;
+    O* C = static_cast<O*>(p.C);
+    const bool whole = reinterpret_cast<uintptr_t>(C) % 16 == 0 && (p.ldc * int64_t(sizeof(O))) % 16 == 0;
+#pragma unroll
+    for (int q = 0; q < kRows * kPieces / 64; ++q) {
+        const uint32_t piece = 64u * q + lane, row = piece / kPieces, col = piece % kPieces * kPer;
+        const uint8_t* from = ep + row * pitch + col * sizeof(O);
+        if (row >= rows || col >= cols) continue;
+        O* to = C + (row0 + row) * p.ldc + col0 + col;
+        if (whole && col + kPer <= cols) {
+            const uint4 val = *reinterpret_cast<const uint4*>(from);
+            const u32x4 vv = {val.x, val.y, val.z, val.w};
+            __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(to));
+        } else {
+#pragma unroll 1
+            for (uint32_t e = 0; e < kPer && col + e < cols; ++e) to[e] = reinterpret_cast<const O*>(from)[e];
+        }
+    }
+}
+
+// Results of a workgroup's tile, through LDS (whose stages are free now), 16
+// rows of the wave tile at a time.
+template <typename O, int MS, int NS, typename P>
+__device__ __forceinline__ void store_tile(const I8Args& p, const v4i (&acc)[MS][NS], uint8_t* lds, const RowTile& r,
+                                           int64_t n0, uint32_t rows, uint32_t cols, uint32_t wave, uint32_t wm,
+                                           uint32_t wn, bool zero) {
+    constexpr int kPitch = 16 * NS * int(sizeof(O)) + 16;
+    static_assert(P::kWaves * 16 * kPitch <= int(P::kScales), "result staging");
+    const uint32_t lane = threadIdx.x & 63u, c0 = wn * 16u * NS;
+    const float* sc = reinterpret_cast<const float*>(lds + P::kScales);
+    uint8_t* ep = lds + wave * (16 * kPitch);
+    float sb[NS], bi[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        sb[j] = sc[P::kTM + c0 + 16u * j + (lane & 15u)];
+        bi[j] = sc[P::kTM + P::kTN + c0 + 16u * j + (lane & 15u)];
+    }
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+        const uint32_t r0 = wm * 16u * MS + 16u * i;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const uint32_t row = 4u * (lane >> 4) + v;
+            const float sa = sc[r0 + row];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                float x = float(acc[i][j][v]) * sa;
+                x = p.bias ? __builtin_fmaf(x, sb[j], bi[j]) : x * sb[j];
+                reinterpret_cast<O*>(ep + row * kPitch)[16 * j + (lane & 15u)] = Out<O>::get(zero ? 0.f : x);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // lgkmcnt(0)
+        __builtin_amdgcn_wave_barrier();
+        store_rows<O, 16 * NS, 16>(p, ep, kPitch, r.m0 + r0, n0 + c0, rows - min(rows, r0), cols - min(cols, c0));
+        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // reads done before the next rows' writes
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <typename O, int MS, int NS, int WM, int WN, bool kStreamB>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_kernel(I8Args p) {
     using P = Pipe<MS, NS, WM, WN>;
-    constexpr int kEsz = int(sizeof(O));
-    constexpr int kPitch = 16 * NS * kEsz + 16;                             // staged result row, bytes
     __shared__ __attribute__((aligned(16))) uint8_t lds[P::kLds];
-    static_assert(P::kWaves * 16 * kPitch <= int(P::kScales), "result staging");
 
     const uint32_t t = threadIdx.x, lane = t & 63u;
     const uint32_t wave = uint32_t(uniform(int32_t(t >> 6)));
     const uint32_t wm = wave / WN, wn = wave % WN;
 
-    // Workgroups are dealt to the 8 XCDs in turn, each with its own L2.  Row
-    // groups: XCD x takes a contiguous eighth of the covered row tiles, all
-    // column tiles of a row tile in a row, then its eighth of the tail.
     RowTile r;
     uint32_t tn;
-    bool zero = false;
-    if (p.offs != nullptr) {
-        const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3, lr = j / p.tiles_n;
-        tn = j - lr * p.tiles_n;
-        uint32_t cov, all;
-        count_tiles<P::kTM>(p.offs, p.G, p.M, &cov, &all);
-        const uint32_t tail = all - cov;
-        const uint32_t c0 = uint32_t(uint64_t(cov) * xcd / 8u), c1 = uint32_t(uint64_t(cov) * (xcd + 1u) / 8u);
-        const uint32_t t0 = cov + uint32_t(uint64_t(tail) * xcd / 8u), t1 = cov + uint32_t(uint64_t(tail) * (xcd + 1u) / 8u);
-        uint32_t tm;
-        if (lr < c1 - c0) tm = c0 + lr;
-        else if (lr < (c1 - c0) + (t1 - t0)) tm = t0 + (lr - (c1 - c0));
-        else return;                                                        // uniform
-        if (!find_tile<P::kTM>(p.offs, p.G, p.M, tm, &r)) return;
-        zero = r.g >= p.G;
-    } else {
-        r.m0 = int64_t(blockIdx.x % p.tiles_m) * P::kTM;
-        r.m1 = p.M;
-        r.g = 0;
-        tn = blockIdx.x / p.tiles_m;
-    }
+    if (!place_tile<P::kTM>(p, &r, &tn)) return;                            // uniform
+    const bool zero = p.offs != nullptr && r.g >= p.G;
     const int64_t n0 = int64_t(tn) * P::kTN;
     const uint32_t rows = uint32_t(min(int64_t(P::kTM), r.m1 - r.m0)), cols = uint32_t(min(int64_t(P::kTN), p.N - n0));
     const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs) + n0 * p.ldb;
@@ -611,15 +692,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_ke
 #pragma unroll
     for (uint32_t s = 0; s + 1 < uint32_t(P::kStages); ++s)
         if (s < n) issue(s, s);
-    {
-        // the tile's scales and bias, while the first stage is on its way
-        float* sc = reinterpret_cast<float*>(lds + P::kScales);
-        if (t < uint32_t(P::kTM)) sc[t] = p.sA[r.m0 + min(t, rows - 1u)];
-        if (t < uint32_t(P::kTN)) {
-            sc[P::kTM + t] = sB[min(t, cols - 1u)];
-            sc[P::kTM + P::kTN + t] = p.bias ? p.bias[n0 + min(t, cols - 1u)] : 0.f;
-        }
-    }
+    load_scales<P>(p, lds, sB, r, n0, rows, cols);                          // while the first stage is on its way
     uint32_t stage = 0;
     for (uint32_t s = 0; s < n; ++s) {
         if constexpr (P::kStages == 3) {
@@ -665,54 +738,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_ke
     }
     __syncthreads();
 
-    // ---- results through LDS, 16 rows of the wave tile at a time ----
-    const float* sc = reinterpret_cast<const float*>(lds + P::kScales);
-    uint8_t* ep = lds + wave * (16 * kPitch);
-    constexpr int kPieces = 16 * NS * kEsz / 16;                            // 16-byte pieces per staged row
-    O* C = static_cast<O*>(p.C);
-    const bool whole = reinterpret_cast<uintptr_t>(C) % 16 == 0 && (p.ldc * kEsz) % 16 == 0;
-    float sb[NS], bi[NS];
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const uint32_t c = wn * 16u * NS + 16u * j + (lane & 15u);
-        sb[j] = sc[P::kTM + c];
-        bi[j] = sc[P::kTM + P::kTN + c];
-    }
-#pragma unroll
-    for (int i = 0; i < MS; ++i) {
-        const uint32_t r0 = wm * 16u * MS + 16u * i;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t row = 4u * (lane >> 4) + v;
-            const float sa = sc[r0 + row];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                float x = float(acc[i][j][v]) * sa;
-                x = p.bias ? __builtin_fmaf(x, sb[j], bi[j]) : x * sb[j];
-                reinterpret_cast<O*>(ep + row * kPitch)[16 * j + (lane & 15u)] = Out<O>::get(zero ? 0.f : x);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // lgkmcnt(0)
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int q = 0; q < 16 * kPieces / 64; ++q) {
-            const uint32_t piece = 64u * q + lane, row = piece / kPieces, pc = piece % kPieces;
-            const uint32_t col = wn * 16u * NS + pc * (16 / kEsz);
-            const uint8_t* from = ep + row * kPitch + 16u * pc;
-            if (r0 + row >= rows || col >= cols) continue;
-            O* to = C + (r.m0 + r0 + row) * p.ldc + n0 + col;
-            if (whole && col + 16 / kEsz <= cols) {
-                const uint4 val = *reinterpret_cast<const uint4*>(from);
-                const u32x4 vv = {val.x, val.y, val.z, val.w};
-                __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(to));
-            } else {
-                for (uint32_t e = 0; e < 16 / kEsz && col + e < cols; ++e) to[e] = reinterpret_cast<const O*>(from)[e];
-            }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);                                 // reads done before the next rows' writes
-        __builtin_amdgcn_wave_barrier();
-    }
+    store_tile<O, MS, NS, P>(p, acc, lds, r, n0, rows, cols, wave, wm, wn, zero);
 }
 
 // Workgroups of a pipelined product.
@@ -756,31 +782,43 @@ hipError_t launch_tiles(I8Args& p, hipStream_t stream) {
 enum class Kind { kStream, kTiles, kPipe };
 struct Form {
     Kind kind;
-    int ms, ns;                  // kStream: 16-row sub-tiles; kPipe: 0 = 256 x 256, 1 = 128 x 256
+    int ms, ns;                  // kStream: 16-row sub-tiles; kPipe: ms 64-row units (1, 2 or 4) by 256 columns
     uint64_t threads;            // of the grid
 };
 
 // pipe: the operands are whole aligned 16-byte pieces.
+//
+// Row groups, by the mean rows of a group (64 experts of [2048, 5120], group
+// sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows, and streamed):
+//   rows    4: 108.0  117.6           145.5       rows  48: 141.8  147.3  156.3  266.1
+//   rows   16: 107.6  113.9           186.6       rows 128: 234.1  173.5  201.1
+//   rows   24: 134.7  113.1  159.4    204.1       rows 192:        229.1  214.0
+//   rows   32: 135.3  115.0  153.9    217.3       rows 384:        394.6  320.1
+// (the 671 MB of weights alone take 108 us at 6.2 TB/s).  Groups of unaligned
+// operands are streamed while they are small.
 Form choose(int64_t M, int64_t N, bool groups, int32_t G, bool pipe) {
     auto stream = [&](int ms, int ns, int waves) {
         return Form{Kind::kStream, ms, ns,
                     uint64_t(tile_bound(M, 16 * ms, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 64u * uint64_t(waves)};
     };
-    auto tiles = [&]() {
+    auto piped = [&](int units) {
         int64_t tm, tn;
-        if (pipe && groups) return Form{Kind::kPipe, 1, 0, pipe_blocks<4, 4, 2, 4>(M, N, groups, G, &tm, &tn) * 512};
-        if (pipe) return Form{Kind::kPipe, 0, 0, pipe_blocks<4, 8, 4, 2>(M, N, groups, G, &tm, &tn) * 512};
-        return Form{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
+        const uint64_t blocks = units == 1   ? pipe_blocks<2, 4, 2, 4>(M, N, groups, G, &tm, &tn)
+                                : units == 2 ? pipe_blocks<4, 4, 2, 4>(M, N, groups, G, &tm, &tn)
+                                             : pipe_blocks<4, 8, 4, 2>(M, N, groups, G, &tm, &tn);
+        return Form{Kind::kPipe, units, 0, blocks * 512};
     };
+    const Form tiles{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
     if (groups) {
         const int64_t rows = (M + G - 1) / G;
+        if (pipe) return piped(rows <= 16 ? 1 : rows <= 160 ? 2 : 4);
         if (rows <= 8) return stream(1, 2, 8);
         if (rows <= 20) return stream(2, 2, 8);
         if (rows <= 48) return stream(4, 2, 8);
-        return tiles();
+        return tiles;
     }
     if (M <= 16) return N >= 16384 ? stream(1, 2, 8) : stream(1, 1, 8);
-    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return tiles();
+    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return pipe ? piped(4) : tiles;
     return ((M + 63) / 64) * ((N + 63) / 64) >= 192 ? stream(4, 4, 4) : stream(2, 2, 8);
 }
 
@@ -793,8 +831,14 @@ bool pipe_fits(const I8Args& p) {
 template <typename O>
 hipError_t launch(I8Args& p, hipStream_t stream) {
     const Form f = choose(p.M, p.N, p.offs != nullptr, p.G, pipe_fits(p));
-    if (f.kind == Kind::kPipe)
-        return f.ms ? launch_pipe<O, 4, 4, 2, 4, true>(p, stream) : launch_pipe<O, 4, 8, 4, 2, false>(p, stream);
+    if (f.kind == Kind::kPipe) {
+        // experts' weights pass through each L2 about once (measured: 113 us with
+        // the hint, 126 without, at 24 rows a group); dense tiles meet in the L2
+        // (428 us without, 470 with it, for 8192 cubed)
+        if (f.ms == 1) return launch_pipe<O, 2, 4, 2, 4, true>(p, stream);
+        if (f.ms == 2) return launch_pipe<O, 4, 4, 2, 4, true>(p, stream);
+        return p.offs ? launch_pipe<O, 4, 8, 4, 2, true>(p, stream) : launch_pipe<O, 4, 8, 4, 2, false>(p, stream);
+    }
     if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
     switch (f.ms * 8 + f.ns) {
         case 8 + 1: return launch_stream<O, 1, 1, 8, 8, void>(p, stream);
