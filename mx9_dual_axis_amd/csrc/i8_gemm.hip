@@ -245,108 +245,43 @@ __global__ __launch_bounds__(256, 2) void i8_gemm_kernel(I8Args p) {
 // before the first is multiplied.  With one to a few tokens this reads the
 // weights once at the rate of memory; with more it is used while whole tiles
 // would leave most CUs without work.
-//
-// X != void: A is not codes but the activations themselves (float or bf16
-// bits): every workgroup quantizes the few rows into LDS, after its first
-// weights are under way, which saves a kernel and its wait.
-constexpr int kFuseBytes = 32 * 1024;    // of activations at most
-
-template <typename X> struct Raw;
-template <> struct Raw<void> {
-    using T = float;
-    static constexpr int kPer = 0;
-};
-template <> struct Raw<float> {
-    using T = float;
-    static constexpr int kPer = 4;
-    static __device__ __forceinline__ float get(const uint32_t (&w)[4], int e) { return __uint_as_float(w[e]); }
-};
-template <> struct Raw<uint16_t> {
-    using T = uint16_t;
-    static constexpr int kPer = 8;
-    static __device__ __forceinline__ float get(const uint32_t (&w)[4], int e) {
-        return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-    }
-};
-
-template <typename X>
-__device__ __forceinline__ void quantize_to_lds(const I8Args& p, uint8_t* codes, uint32_t pitch, float* scales,
-                                                uint32_t* maxes, uint32_t t, uint32_t threads) {
-    constexpr int kPer = Raw<X>::kPer, kHold = 4;          // kFuseBytes / 16 pieces over 512 threads
-    const uint32_t per_row = uint32_t(p.K) / kPer, pieces = per_row * uint32_t(p.M);
-    uint32_t w[kHold][4];
-    if (t < 16) maxes[t] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const uint32_t c = t + uint32_t(i) * threads;
-        if (c < pieces) {
-            const uint32_t row = c / per_row;
-            __builtin_memcpy(w[i], reinterpret_cast<const char*>(p.A) +
-                                       (int64_t(row) * p.lda + int64_t(c - row * per_row) * kPer) * int64_t(sizeof(X)), 16);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const uint32_t c = t + uint32_t(i) * threads;
-        uint32_t m = 0;
-        if (c < pieces) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) m = max(m, __float_as_uint(Raw<X>::get(w[i], e)) & 0x7FFFFFFFu);
-        }
-        if (per_row % 64 == 0) {                           // a wave's pieces are one row's
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), d, 64)));
-            if ((t & 63u) == 0 && c < pieces) atomicMax(&maxes[c / per_row], m);
-        } else if (c < pieces) {
-            atomicMax(&maxes[c / per_row], m);
-        }
-    }
-    __syncthreads();
-    if (t < uint32_t(p.M)) {
-        const uint32_t m = maxes[t];
-        scales[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 127.f * 0x1p-126f) / 127.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const uint32_t c = t + uint32_t(i) * threads;
-        if (c >= pieces) continue;
-        const uint32_t row = c / per_row, m = maxes[row];
-        const float inv = 127.f / fmaxf(__uint_as_float(m), 127.f * 0x1p-126f);
-        uint32_t o[kPer / 4];
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v |= uint32_t(int(rintf(Raw<X>::get(w[i], 4 * q + e) * inv)) & 255) << (8 * e);
-            o[q] = m >= 0x7F800000u ? 0u : v;
-        }
-        uint32_t* at = reinterpret_cast<uint32_t*>(codes + row * pitch + (c - row * per_row) * kPer);
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) at[q] = o[q];
-    }
-    // zeros up to whole steps
-    const uint32_t pad = (64u - uint32_t(p.K) % 64u) % 64u / 16u;
-    for (uint32_t c = t; c < pad * uint32_t(p.M); c += threads)
-        *reinterpret_cast<uint4*>(codes + (c / pad) * pitch + uint32_t(p.K) + 16u * (c % pad)) = uint4{0, 0, 0, 0};
-    __syncthreads();
-}
-
 __device__ __forceinline__ v4i load16(const int8_t* p) {
     v4i v;
     __builtin_memcpy(&v, p, 16);
     return v;
 }
 
-template <typename O, int MS, int NS, int kW, int kU, typename X>
-__global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
-    constexpr bool kFuse = Raw<X>::kPer != 0;
+// The sums of a workgroup's waves, which split the contraction, meet in LDS
+// and become C's (16 MS) x (16 NS) tile.
+template <typename O, int MS, int NS, int kW>
+__device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[MS][NS], int* sums, const RowTile& r,
+                                           int64_t n0, const float* sB, const float* sA, bool zero) {
     constexpr int kRegs = MS * NS * 4;
-    constexpr int kSums = kW * kRegs * 256, kCodes = kFuse ? kFuseBytes / int(sizeof(typename Raw<X>::T)) + 16 * 80 : 0;
-    __shared__ __attribute__((aligned(16))) uint8_t dyn[kSums > kCodes ? kSums : kCodes];   // sums, the codes before them
-    __shared__ float scales[16];
-    __shared__ uint32_t maxes[16];
+    const uint32_t t = threadIdx.x, lane = t & 63u, wave = uint32_t(uniform(int32_t(t >> 6)));
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sums[(wave * kRegs + (i * NS + j) * 4 + v) * 64 + lane] = acc[i][j][v];
+    __syncthreads();
+    O* C = static_cast<O*>(p.C);
+    for (uint32_t q = wave; q < uint32_t(kRegs); q += kW) {
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) sum += sums[(w * kRegs + q) * 64 + lane];
+        const uint32_t i = q / (4 * NS), j = q / 4 % NS, v = q & 3u;
+        const int64_t row = r.m0 + 16 * i + 4 * (lane >> 4) + v, col = n0 + 16 * j + (lane & 15u);
+        if (row >= r.m1 || col >= p.N) continue;
+        float x = float(sum) * sA[row];
+        x = p.bias ? __builtin_fmaf(x, sB[col], p.bias[col]) : x * sB[col];
+        C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : x);
+    }
+}
+
+template <typename O, int MS, int NS, int kW, int kU>
+__global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
+    __shared__ __attribute__((aligned(16))) int sums[kW * MS * NS * 4 * 64];
     const uint32_t t = threadIdx.x, lane = t & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = uint32_t(uniform(int32_t(t >> 6)));
     const uint32_t tm = p.offs ? blockIdx.x / p.tiles_n : blockIdx.x % p.tiles_m;
@@ -361,12 +296,10 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
     const int64_t per = (p.K + kW * 128 - 1) / (kW * 128) * 128;
     const int64_t k0 = zero ? p.K : min(int64_t(wave) * per, p.K), k1 = min(k0 + per, p.K);
     const int8_t *pa[MS], *pb[NS];
-    const uint32_t pitch = kFuse ? (uint32_t(p.K) + 63u) / 64u * 64u + 16u : 0u;
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
         const int64_t row = r.m0 + 16 * i + l16;
-        if constexpr (!kFuse) pa[i] = p.A + (row < r.m1 ? row : r.m1 - 1) * p.lda + 16 * g;
-        else pa[i] = reinterpret_cast<const int8_t*>(dyn) + uint32_t(row < p.M ? row : p.M - 1) * pitch + 16 * g;
+        pa[i] = p.A + (row < r.m1 ? row : r.m1 - 1) * p.lda + 16 * g;
     }
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
@@ -379,21 +312,13 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
 #pragma unroll
         for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
-    v4i b[kU][NS];
     int64_t k = k0;
-    const bool first = k + 64 * kU <= k1;
-    auto load_b = [&]() {
+    for (; k + 64 * kU <= k1; k += 64 * kU) {
+        v4i b[kU][NS];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int j = 0; j < NS; ++j) b[u][j] = load16(pb[j] + k + 64 * u);
-    };
-    if constexpr (kFuse) {
-        if (first) load_b();
-        quantize_to_lds<typename Raw<X>::T>(p, dyn, pitch, scales, maxes, t, 64 * kW);
-    }
-    for (; k + 64 * kU <= k1; k += 64 * kU) {
-        if (!kFuse || k != k0) load_b();
         v4i a[kU][MS];
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -410,7 +335,7 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
     for (; k < k1; k += 64) {
         v4i a[MS], c[NS];
 #pragma unroll
-        for (int i = 0; i < MS; ++i) a[i] = kFuse ? load16(pa[i] + k) : load_codes(pa[i] - 16 * g, k + 16 * g, p.K);
+        for (int i = 0; i < MS; ++i) a[i] = load_codes(pa[i] - 16 * g, k + 16 * g, p.K);
 #pragma unroll
         for (int j = 0; j < NS; ++j) c[j] = load_codes(pb[j] - 16 * g, k + 16 * g, p.K);
 #pragma unroll
@@ -419,29 +344,7 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
             for (int j = 0; j < NS; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], c[j], acc[i][j], 0, 0, 0);
     }
 
-    // ---- the waves' sums ----
-    if (kFuse) __syncthreads();                                            // the codes are read
-    int* red = reinterpret_cast<int*>(dyn);
-#pragma unroll
-    for (int i = 0; i < MS; ++i)
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) red[(wave * kRegs + (i * NS + j) * 4 + v) * 64 + lane] = acc[i][j][v];
-    __syncthreads();
-    O* C = static_cast<O*>(p.C);
-    for (uint32_t q = wave; q < uint32_t(kRegs); q += kW) {
-        int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) sum += red[(w * kRegs + q) * 64 + lane];
-        const uint32_t i = q / (4 * NS), j = q / 4 % NS, v = q & 3u;
-        const int64_t row = r.m0 + 16 * i + 4 * g + v, col = n0 + 16 * j + l16;
-        if (row >= r.m1 || col >= p.N) continue;
-        const float sa = kFuse ? scales[row] : p.sA[row];
-        float x = float(sum) * sa;
-        x = p.bias ? __builtin_fmaf(x, sB[col], p.bias[col]) : x * sB[col];
-        C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : x);
-    }
+    store_sums<O, MS, NS, kW>(p, acc, sums, r, n0, sB, p.sA, zero);
 }
 
 // ---- many tiles, aligned operands: pipelined through LDS ----
@@ -484,18 +387,18 @@ __device__ __forceinline__ void pipe_sync() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-template <int MS, int NS, int WM, int WN>
+template <int MS, int NS, int WM, int WN, int ST>
 struct Pipe {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int kTM = 16 * MS * WM, kTN = 16 * NS * WN;
     static constexpr int kLA = kTM / 8 / kWaves, kLB = kTN / 8 / kWaves;    // loads per wave and step
     static constexpr uint32_t kB = uint32_t(kTM) * 128, kStage = kB + uint32_t(kTN) * 128;
-    static constexpr int kStages = (152 * 1024) / kStage >= 3 ? 3 : 2;
+    static constexpr int kStages = ST;
     static constexpr uint32_t kScales = kStages * kStage;                   // sA, sB, bias of the tile
     static constexpr uint32_t kLds = kScales + uint32_t(kTM + 2 * kTN) * 4;
     static constexpr int kLoads = kLA + kLB;
     static_assert(kLA * kWaves * 8 == kTM && kLB * kWaves * 8 == kTN && kLds <= 160 * 1024, "tile");
-    static_assert(kThreads >= kTM && kThreads >= kTN, "scales: one per thread");
+    static_assert(kThreads >= kTM && kThreads >= kTN && (kStages - 2) * kLoads < 64, "scales: one per thread; vmcnt");
 };
 
 __device__ __forceinline__ v8i fragment(const v4i* tile, uint32_t row, uint32_t lane) {
@@ -640,9 +543,9 @@ __device__ __forceinline__ void store_tile(const I8Args& p, const v4i (&acc)[MS]
     }
 }
 
-template <typename O, int MS, int NS, int WM, int WN, bool kStreamB>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_kernel(I8Args p) {
-    using P = Pipe<MS, NS, WM, WN>;
+template <typename O, int MS, int NS, int WM, int WN, int ST, bool kStreamB>
+__global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
+    using P = Pipe<MS, NS, WM, WN, ST>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[P::kLds];
 
     const uint32_t t = threadIdx.x, lane = t & 63u;
@@ -695,12 +598,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_ke
     load_scales<P>(p, lds, sB, r, n0, rows, cols);                          // while the first stage is on its way
     uint32_t stage = 0;
     for (uint32_t s = 0; s < n; ++s) {
-        if constexpr (P::kStages == 3) {
-            if (s + 1 < n) pipe_sync<P::kLoads>();
-            else pipe_sync<0>();
-        } else {
-            pipe_sync<0>();
-        }
+        // step s has arrived; the kStages - 2 after it may be under way (near the
+        // end, where fewer are, all are waited for)
+        if (P::kStages > 2 && s + P::kStages - 2 < n) pipe_sync<(P::kStages - 2) * P::kLoads>();
+        else pipe_sync<0>();
         if (s + P::kStages - 1 < n) {
             const uint32_t free = stage == 0 ? uint32_t(P::kStages - 1) : stage - 1u;
             issue(s + P::kStages - 1, free);
@@ -741,32 +642,233 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN >= 8 ? 2 : 1) void i8_pipe_ke
     store_tile<O, MS, NS, P>(p, acc, lds, r, n0, rows, cols, wave, wm, wn, zero);
 }
 
-// Workgroups of a pipelined product.
-template <int MS, int NS, int WM, int WN>
-uint64_t pipe_blocks(int64_t M, int64_t N, bool groups, int32_t G, int64_t* tiles_m, int64_t* tiles_n) {
-    using P = Pipe<MS, NS, WM, WN>;
-    *tiles_m = tile_bound(M, P::kTM, groups, G);
-    *tiles_n = (N + P::kTN - 1) / P::kTN;
-    // an XCD's share: at most a ceiling of the covered tiles and one of the tail's
-    return groups ? uint64_t(8 * ((*tiles_m + 7) / 8 + 1)) * uint64_t(*tiles_n) : uint64_t(*tiles_m) * uint64_t(*tiles_n);
+// ---- up to 16 rows, aligned operands: a ring of LDS slots for each wave ----
+//
+// One workgroup of kW waves computes 16 x (16 NS) of C.  Wave w takes the steps
+// (128 codes) w, w + kW, ... of the contraction for itself: its loads go
+// straight into its own ring of kS slots, eight whole 128-byte lines of the
+// operands at a time, and it waits for nothing but them, so up to kS steps of
+// every wave are under way at any moment and there is no barrier before the
+// sums meet.  (Fragments loaded into registers touch sixteen 64-byte pieces per
+// quarter wave instead, four times the cache lookups: RING.)
+//
+// X != void: A is not codes but the activations themselves (float or bf16
+// bits): every workgroup quantizes the few rows into LDS, with its first
+// weights under way, which saves a kernel and its wait.
+constexpr int kFuseBytes = 16 * 1024;    // of activations at most
+
+template <typename X> struct Raw;
+template <> struct Raw<void> {
+    using T = float;
+    static constexpr int kPer = 0;
+};
+template <> struct Raw<float> {
+    using T = float;
+    static constexpr int kPer = 4;
+    static __device__ __forceinline__ float get(const v4i& w, int e) { return __int_as_float(w[e]); }
+};
+template <> struct Raw<uint16_t> {
+    using T = uint16_t;
+    static constexpr int kPer = 8;
+    static __device__ __forceinline__ float get(const v4i& w, int e) {
+        return __uint_as_float(e & 1 ? uint32_t(w[e >> 1]) & 0xFFFF0000u : uint32_t(w[e >> 1]) << 16);
+    }
+};
+
+// A barrier that leaves loads on their way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {                    // over 16 lanes, by DPP rotations
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x128, 0xF, 0xF, false)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x124, 0xF, 0xF, false)));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x122, 0xF, 0xF, false)));
+    return max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x121, 0xF, 0xF, false)));
 }
 
-template <typename O, int MS, int NS, int WM, int WN, bool kStreamB>
-hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
-    int64_t tm, tn;
-    const uint64_t blocks = pipe_blocks<MS, NS, WM, WN>(p.M, p.N, p.offs != nullptr, p.G, &tm, &tn);
-    p.tiles_m = uint32_t(tm);
-    p.tiles_n = uint32_t(tn);
-    hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, kStreamB>), dim3(uint32_t(blocks)), dim3(64 * WM * WN), 0,
+// Rows of activations to codes (rows `pitch` bytes apart, zeros up to whole
+// 128-code steps) and scales in LDS.  The activations go to LDS themselves
+// first (`raw`), every thread's pieces to where it reads them, and `then` puts
+// the weights on their way right behind them; `arrived` waits for the former.
+template <typename X, int kThr, typename F, typename W>
+__device__ __forceinline__ void quantize_to_lds(const I8Args& p, uint8_t* raw, uint8_t* codes, uint32_t pitch,
+                                                float* scales, uint32_t* maxes, F&& then, W&& arrived) {
+    constexpr int kPer = Raw<X>::kPer, kHold = kFuseBytes / 16 / kThr;
+    const uint32_t t = threadIdx.x, lane = t & 63u, wave = uint32_t(uniform(int32_t(t >> 6)));
+    const uint32_t per_row = uint32_t(p.K) / kPer, pieces = per_row * uint32_t(p.M), M = uint32_t(p.M);
+    const v4i rx = pipe_rsrc(p.A, uint64_t((p.M - 1) * p.lda + p.K) * sizeof(X));
+    const uint32_t base = uint32_t(reinterpret_cast<uintptr_t>(raw)) + 1024u * wave;
+    uint32_t row[kHold], piece[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (uint32_t(i * kThr) >= pieces) break;                            // uniform
+        const uint32_t c = min(t + uint32_t(i * kThr), pieces - 1u);        // past the last: that one again
+        row[i] = c / per_row;
+        piece[i] = c - row[i] * per_row;
+        pipe_load16(rx, base + uint32_t(i * kThr) * 16u, (row[i] * uint32_t(p.lda) + piece[i] * kPer) * sizeof(X), 0u);
+    }
+    then();
+    if (t < M) maxes[t] = 0;
+    lds_barrier();
+    arrived();
+    v4i w[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (uint32_t(i * kThr) >= pieces) break;
+        w[i] = *reinterpret_cast<const v4i*>(raw + uint32_t(i * kThr) * 16u + 1024u * wave + 16u * lane);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) m = max(m, __float_as_uint(Raw<X>::get(w[i], e)) & 0x7FFFFFFFu);
+        if (per_row % 16u == 0) {                                           // 16 lanes hold one row's pieces
+            m = row_max(m);
+            if ((lane & 15u) == 0) atomicMax(&maxes[row[i]], m);
+        } else {
+            atomicMax(&maxes[row[i]], m);
+        }
+    }
+    lds_barrier();
+    if (t < M) {
+        const uint32_t m = maxes[t];
+        scales[t] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__uint_as_float(m), 127.f * 0x1p-126f) / 127.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (uint32_t(i * kThr) >= pieces) break;
+        const uint32_t m = maxes[row[i]];
+        const float inv = 127.f / fmaxf(__uint_as_float(m), 127.f * 0x1p-126f);
+        uint32_t* at = reinterpret_cast<uint32_t*>(codes + row[i] * pitch + piece[i] * kPer);
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v |= uint32_t(int(rintf(Raw<X>::get(w[i], 4 * q + e) * inv)) & 255) << (8 * e);
+            at[q] = m >= 0x7F800000u ? 0u : v;
+        }
+    }
+    const uint32_t pad = (128u - uint32_t(p.K) % 128u) % 128u / 16u;
+    for (uint32_t c = t; c < pad * M; c += kThr)
+        *reinterpret_cast<v4i*>(codes + (c / pad) * pitch + uint32_t(p.K) + 16u * (c % pad)) = v4i{0, 0, 0, 0};
+    lds_barrier();
+}
+
+template <typename O, int NS, int kW, int kS, typename X>
+__global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
+    constexpr bool kFuse = Raw<X>::kPer != 0;
+    constexpr int kLA = kFuse ? 0 : 2, kLB = 2 * NS, kLoads = kLA + kLB;
+    constexpr uint32_t kSlot = uint32_t(kLoads) * 1024u, kRing = kW * kS * kSlot;
+    // codes: rows of a multiple of 128, 16 more against bank conflicts
+    constexpr uint32_t kCodes = kFuse ? kFuseBytes / uint32_t(sizeof(typename Raw<X>::T)) + 16 * 128 : 0u;
+    constexpr uint32_t kRaw = kFuse ? kFuseBytes : 0u;
+    static_assert(kRing + kCodes + kRaw <= 160 * 1024 - 256 && kRing >= kW * NS * 1024u && kS * kLoads < 64, "LDS, vmcnt");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + kCodes + kRaw];
+    __shared__ float scales[kFuse ? 16 : 1];
+    __shared__ uint32_t maxes[kFuse ? 16 : 1];
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = uint32_t(uniform(int32_t(threadIdx.x >> 6)));
+    const int64_t n0 = int64_t(blockIdx.x) * (16 * NS);
+    const RowTile r{0, p.M, 0};
+    const uint32_t K = uint32_t(p.K), steps = (K + 127u) / 128u;
+    const uint32_t mine = steps > wave ? (steps - wave + kW - 1u) / kW : 0u;
+    const uint32_t rows = uint32_t(p.M), cols = uint32_t(min(int64_t(16 * NS), p.N - n0));
+    const uint32_t lda = uint32_t(p.lda), ldb = uint32_t(p.ldb);
+    const uint32_t lr = lane >> 3, lc = 16u * ((lane & 7u) ^ lr);
+    const v4i ra = pipe_rsrc(p.A, kFuse ? 0 : uint64_t(rows - 1u) * lda + K);
+    const v4i rb = pipe_rsrc(p.B + n0 * p.ldb, uint64_t(cols - 1u) * ldb + K);
+    uint32_t va[2], vb[kLB];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) va[q] = min(8u * q + lr, rows - 1u) * lda + lc;
+#pragma unroll
+    for (int q = 0; q < kLB; ++q) vb[q] = min(8u * q + lr, cols - 1u) * ldb + lc;
+    const uint32_t cut = K % 128u != 0 && lc >= K % 128u ? lc : 0u;          // the last step's pieces past K read piece 0
+    const uint32_t ring = uint32_t(reinterpret_cast<uintptr_t>(lds)) + wave * (kS * kSlot);
+    auto issue = [&](uint32_t i, uint32_t slot) {
+        const uint32_t step = wave + kW * i, back = step + 1u == steps ? cut : 0u, at = ring + slot * kSlot;
+#pragma unroll
+        for (int q = 0; q < kLB; ++q) pipe_load16_nt(rb, at + 1024u * q, vb[q] - back, step * 128u);
+#pragma unroll
+        for (int q = 0; q < kLA; ++q) pipe_load16(ra, at + 1024u * (kLB + q), va[q] - back, step * 128u);
+    };
+    auto fill = [&]() {
+#pragma unroll
+        for (uint32_t i = 0; i < uint32_t(kS); ++i)
+            if (i < mine) issue(i, i);
+    };
+    const uint32_t pitch = (K + 127u) / 128u * 128u + 16u;
+    uint8_t* codes = lds + kRing;
+    if constexpr (kFuse) {
+        quantize_to_lds<X, 64 * kW>(p, codes + kCodes, codes, pitch, scales, maxes, fill, [&]() {
+            if (mine >= uint32_t(kS)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kS * kLoads) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        });
+    } else {
+        fill();
+    }
+
+    v4i acc[1][NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) acc[0][j] = v4i{0, 0, 0, 0};
+    uint32_t slot = 0;
+    for (uint32_t i = 0; i < mine; ++i) {
+        // step i has arrived; near the end, where fewer are under way, all are waited for
+        if (i + kS <= mine) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kS - 1) * kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t step = wave + kW * i;
+        const uint8_t* at = lds + wave * (kS * kSlot) + slot * kSlot;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t piece = 4u * h + g;
+            v4i a;
+            if constexpr (kFuse) {
+                a = *reinterpret_cast<const v4i*>(codes + min(l16, rows - 1u) * pitch + step * 128u + 16u * piece);
+            } else {
+                a = reinterpret_cast<const v4i*>(at + 1024u * kLB)[l16 * 8u + (piece ^ (l16 & 7u))];
+                // codes past K: cleared, and any integer times 0 is 0
+                if (step + 1u == steps && step * 128u + 16u * piece >= K) a = v4i{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                const v4i b = reinterpret_cast<const v4i*>(at)[(16u * j + l16) * 8u + (piece ^ (l16 & 7u))];
+                acc[0][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc[0][j], 0, 0, 0);
+            }
+        }
+        if (i + kS < mine) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");               // the slot is read
+            issue(i + kS, slot);
+        }
+        slot = slot + 1u == uint32_t(kS) ? 0u : slot + 1u;
+    }
+    __syncthreads();                                                         // every ring is read
+    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, p.sB, kFuse ? scales : p.sA, false);
+}
+
+template <typename O, int NS, int kW, int kS, typename X>
+hipError_t launch_ring(I8Args& p, hipStream_t stream) {
+    hipLaunchKernelGGL((i8_ring_kernel<O, NS, kW, kS, X>), dim3(uint32_t((p.N + 16 * NS - 1) / (16 * NS))), dim3(64 * kW), 0,
                        stream, p);
     return hipGetLastError();
 }
 
-template <typename O, int MS, int NS, int kW, int kU, typename X>
+// Row tiles that a grouped grid has room for: an XCD's share is at most a
+// ceiling of the covered tiles and one of the tail's.
+int64_t group_tiles(int64_t tiles_m) { return 8 * ((tiles_m + 7) / 8 + 1); }
+
+template <typename O, int MS, int NS, int WM, int WN, int ST, bool kStreamB>
+hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
+    using P = Pipe<MS, NS, WM, WN, ST>;
+    const int64_t tm = tile_bound(p.M, P::kTM, p.offs != nullptr, p.G);
+    p.tiles_m = uint32_t(tm);
+    p.tiles_n = uint32_t((p.N + P::kTN - 1) / P::kTN);
+    const uint32_t blocks = uint32_t(p.offs ? group_tiles(tm) : tm) * p.tiles_n;
+    hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, ST, kStreamB>), dim3(blocks), dim3(64 * WM * WN), 0,
+                       stream, p);
+    return hipGetLastError();
+}
+
+template <typename O, int MS, int NS, int kW, int kU>
 hipError_t launch_stream(I8Args& p, hipStream_t stream) {
     p.tiles_m = uint32_t(tile_bound(p.M, 16 * MS, p.offs != nullptr, p.G));
     p.tiles_n = uint32_t((p.N + 16 * NS - 1) / (16 * NS));
-    hipLaunchKernelGGL((i8_stream_kernel<O, MS, NS, kW, kU, X>), dim3(p.tiles_m * p.tiles_n), dim3(64 * kW), 0, stream, p);
+    hipLaunchKernelGGL((i8_stream_kernel<O, MS, NS, kW, kU>), dim3(p.tiles_m * p.tiles_n), dim3(64 * kW), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -778,11 +880,25 @@ hipError_t launch_tiles(I8Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Columns per workgroup: at most 512 workgroups (two of about 64 KiB LDS on
+// each CU) while that is 64 at most.  [8192, 8192] with one row: 16 columns
+// 13.1 us, 32 19.0, 64 15.2; [14336, 4096]: 16 columns 14.7 us, 32 12.8, 64 12.4.
+int ring_columns(int64_t N) { return N <= 16 * 512 ? 1 : (N <= 32 * 512 ? 2 : 4); }
+
+template <typename O, typename X>
+hipError_t ring(I8Args& p, hipStream_t stream) {
+    switch (ring_columns(p.N)) {
+        case 1: return launch_ring<O, 1, 8, 2, X>(p, stream);
+        case 2: return launch_ring<O, 2, 4, 3, X>(p, stream);
+        default: return launch_ring<O, 4, 4, 2, X>(p, stream);
+    }
+}
+
 // Which kernel.
-enum class Kind { kStream, kTiles, kPipe };
+enum class Kind { kStream, kTiles, kRing, kPipe };
 struct Form {
     Kind kind;
-    int ms, ns;                  // kStream: 16-row sub-tiles; kPipe: ms 64-row units (1, 2 or 4) by 256 columns
+    int ms, ns;                  // kStream: 16-row, 16-column sub-tiles of a workgroup; kPipe: 64-row, 64-column units
     uint64_t threads;            // of the grid
 };
 
@@ -796,29 +912,52 @@ struct Form {
 //   rows   32: 135.3  115.0  153.9    217.3       rows 384:        394.6  320.1
 // (the 671 MB of weights alone take 108 us at 6.2 TB/s).  Groups of unaligned
 // operands are streamed while they are small.
-Form choose(int64_t M, int64_t N, bool groups, int32_t G, bool pipe) {
+//
+// Dense: the piped tile with the least ceil(tiles / 256 CUs) (steps t + 1.2
+// us), t the time of one 128-code step: 256 x 256 1.25 us, 128 x 256 0.80,
+// 128 x 128 0.57, 128 x 64 0.51, 64 x 64 0.33.  These were fitted to all five
+// tiles' times over 39 shapes (M 32 to 4096; N, K 14336 x 4096, 8192 x 8192 and
+// 2048 x 5120), where the choice is 1.6% behind the best tile on average and
+// 28% at most.
+Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) {
     auto stream = [&](int ms, int ns, int waves) {
         return Form{Kind::kStream, ms, ns,
                     uint64_t(tile_bound(M, 16 * ms, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 64u * uint64_t(waves)};
     };
-    auto piped = [&](int units) {
-        int64_t tm, tn;
-        const uint64_t blocks = units == 1   ? pipe_blocks<2, 4, 2, 4>(M, N, groups, G, &tm, &tn)
-                                : units == 2 ? pipe_blocks<4, 4, 2, 4>(M, N, groups, G, &tm, &tn)
-                                             : pipe_blocks<4, 8, 4, 2>(M, N, groups, G, &tm, &tn);
-        return Form{Kind::kPipe, units, 0, blocks * 512};
-    };
     const Form tiles{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
+    auto piped = [&](int um, int un) {
+        const int64_t tm = tile_bound(M, 64 * um, groups, G), tn = (N + 64 * un - 1) / (64 * un);
+        return Form{Kind::kPipe, um, un, uint64_t(groups ? group_tiles(tm) : tm) * uint64_t(tn) * 512};
+    };
     if (groups) {
         const int64_t rows = (M + G - 1) / G;
-        if (pipe) return piped(rows <= 16 ? 1 : rows <= 160 ? 2 : 4);
+        if (pipe) return piped(rows <= 16 ? 1 : rows <= 160 ? 2 : 4, 4);
         if (rows <= 8) return stream(1, 2, 8);
         if (rows <= 20) return stream(2, 2, 8);
         if (rows <= 48) return stream(4, 2, 8);
         return tiles;
     }
+    if (pipe) {
+        if (M <= 16) return Form{Kind::kRing, 1, ring_columns(N), uint64_t((N + 15) / 16) * 512};
+        struct Tile {
+            int um, un;
+            double step;
+        };
+        constexpr Tile kTiles[] = {{4, 4, 1.25}, {2, 4, 0.80}, {2, 2, 0.57}, {2, 1, 0.51}, {1, 1, 0.33}};
+        const Tile* best = nullptr;
+        double least = 0;
+        for (const Tile& t : kTiles) {
+            const int64_t n = ((M + 64 * t.um - 1) / (64 * t.um)) * ((N + 64 * t.un - 1) / (64 * t.un));
+            const double cost = double((n + 255) / 256) * (double((K + 127) / 128) * t.step + 1.2);
+            if (!best || cost < least) {
+                best = &t;
+                least = cost;
+            }
+        }
+        return piped(best->um, best->un);
+    }
     if (M <= 16) return N >= 16384 ? stream(1, 2, 8) : stream(1, 1, 8);
-    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return pipe ? piped(4) : tiles;
+    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return tiles;
     return ((M + 63) / 64) * ((N + 63) / 64) >= 192 ? stream(4, 4, 4) : stream(2, 2, 8);
 }
 
@@ -830,31 +969,39 @@ bool pipe_fits(const I8Args& p) {
 
 template <typename O>
 hipError_t launch(I8Args& p, hipStream_t stream) {
-    const Form f = choose(p.M, p.N, p.offs != nullptr, p.G, pipe_fits(p));
+    const Form f = choose(p.M, p.N, p.K, p.offs != nullptr, p.G, pipe_fits(p));
+    if (f.kind == Kind::kRing) return ring<O, void>(p, stream);
     if (f.kind == Kind::kPipe) {
         // experts' weights pass through each L2 about once (measured: 113 us with
         // the hint, 126 without, at 24 rows a group); dense tiles meet in the L2
         // (428 us without, 470 with it, for 8192 cubed)
-        if (f.ms == 1) return launch_pipe<O, 2, 4, 2, 4, true>(p, stream);
-        if (f.ms == 2) return launch_pipe<O, 4, 4, 2, 4, true>(p, stream);
-        return p.offs ? launch_pipe<O, 4, 8, 4, 2, true>(p, stream) : launch_pipe<O, 4, 8, 4, 2, false>(p, stream);
+        if (p.offs) {
+            if (f.ms == 1) return launch_pipe<O, 2, 4, 2, 4, 3, true>(p, stream);
+            if (f.ms == 2) return launch_pipe<O, 4, 4, 2, 4, 3, true>(p, stream);
+            return launch_pipe<O, 4, 8, 4, 2, 2, true>(p, stream);
+        }
+        if (f.ms == 4) return launch_pipe<O, 4, 8, 4, 2, 2, false>(p, stream);
+        if (f.ms == 1) return launch_pipe<O, 1, 2, 4, 2, 4, false>(p, stream);
+        if (f.ns == 4) return launch_pipe<O, 4, 4, 2, 4, 3, false>(p, stream);
+        if (f.ns == 2) return launch_pipe<O, 2, 4, 4, 2, 4, false>(p, stream);
+        return launch_pipe<O, 2, 2, 4, 2, 6, false>(p, stream);
     }
     if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
     switch (f.ms * 8 + f.ns) {
-        case 8 + 1: return launch_stream<O, 1, 1, 8, 8, void>(p, stream);
-        case 8 + 2: return launch_stream<O, 1, 2, 8, 4, void>(p, stream);
-        case 16 + 2: return launch_stream<O, 2, 2, 8, 4, void>(p, stream);
-        case 32 + 2: return launch_stream<O, 4, 2, 8, 2, void>(p, stream);
-        default: return launch_stream<O, 4, 4, 4, 2, void>(p, stream);
+        case 8 + 1: return launch_stream<O, 1, 1, 8, 8>(p, stream);
+        case 8 + 2: return launch_stream<O, 1, 2, 8, 4>(p, stream);
+        case 16 + 2: return launch_stream<O, 2, 2, 8, 4>(p, stream);
+        case 32 + 2: return launch_stream<O, 4, 2, 8, 2>(p, stream);
+        default: return launch_stream<O, 4, 4, 4, 2>(p, stream);
     }
 }
 
 }  // namespace
 
 // The threads of the largest grid that a product of this shape launches.
-uint64_t i8_gemm_threads(int64_t M, int64_t N, bool groups, int32_t G) {
+uint64_t i8_gemm_threads(int64_t M, int64_t N, int64_t K, bool groups, int32_t G) {
     if (M <= 0 || N <= 0) return 0;
-    const uint64_t a = choose(M, N, groups, G, false).threads, b = choose(M, N, groups, G, true).threads;
+    const uint64_t a = choose(M, N, K, groups, G, false).threads, b = choose(M, N, K, groups, G, true).threads;
     return a > b ? a : b;
 }
 
@@ -867,8 +1014,11 @@ hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const i
     return out_dtype == 0 ? launch<float>(p, stream) : launch<__bf16>(p, stream);
 }
 
-bool i8_linear_fuses(int64_t M, int64_t K, int dtype) {
-    return M <= 16 && K > 0 && K % 16 == 0 && M * K * (dtype == 0 ? 4 : 2) <= kFuseBytes;
+bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t K) {
+    const int64_t esz = dtype == 0 ? 4 : 2;
+    return M <= 16 && K > 0 && K % 16 == 0 && M * K * esz <= kFuseBytes && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+           (M == 1 || ld_x * esz % 16 == 0) && (M - 1) * ld_x * esz < (1 << 30) && reinterpret_cast<uintptr_t>(B) % 16 == 0 &&
+           ldb % 16 == 0 && ldb < (1 << 23);
 }
 
 hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, const float* sB,
@@ -879,10 +1029,8 @@ hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const 
     p.sb_gs = 0; p.bias = bias; p.C = C; p.ldc = ldc; p.M = M; p.N = N; p.K = K; p.offs = nullptr; p.G = 0;
     p.tiles_m = p.tiles_n = 0;
     if (dtype == 0)
-        return out_dtype == 0 ? launch_stream<float, 1, 1, 8, 8, float>(p, stream)
-                              : launch_stream<__bf16, 1, 1, 8, 8, float>(p, stream);
-    return out_dtype == 0 ? launch_stream<float, 1, 1, 8, 8, uint16_t>(p, stream)
-                          : launch_stream<__bf16, 1, 1, 8, 8, uint16_t>(p, stream);
+        return out_dtype == 0 ? ring<float, float>(p, stream) : ring<__bf16, float>(p, stream);
+    return out_dtype == 0 ? ring<float, uint16_t>(p, stream) : ring<__bf16, uint16_t>(p, stream);
 }
 
 }  // namespace mxq

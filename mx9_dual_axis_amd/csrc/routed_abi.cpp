@@ -70,7 +70,7 @@ int check_product(const int8_t* B, int64_t ldb, int64_t b_gs, const float* sB, i
     if (some && ((!B && K > 0) || !sB || !C || (groups && !offs))) return MX_E_NULL;
     if (!dtype_ok(out_dtype)) return MX_E_DTYPE;
     if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxCodes || G < 1) return MX_E_SHAPE;
-    if (mxq::i8_gemm_threads(M, N, groups, G) > kMaxThreads) return MX_E_SHAPE;
+    if (mxq::i8_gemm_threads(M, N, K, groups, G) > kMaxThreads) return MX_E_SHAPE;
     if (ldb < K || ldc < N || b_gs < 0 || sb_gs < 0) return MX_E_STRIDE;
     const int64_t esz = elem(out_dtype);
     const uint64_t bb = matrix_bytes(N, K, ldb, 1), cb = matrix_bytes(M, N, ldc, esz);
@@ -234,7 +234,7 @@ int i8_linear(const void* x, int32_t dtype, int64_t ld_x, const int8_t* B, int64
     sp[4] = {addr(x), xb};
     if (outputs_clash(sp, 2, 6)) return MX_E_OVERLAP;
     if (!some) return MX_OK;
-    if (mxq::i8_linear_fuses(M, K, dtype))
+    if (mxq::i8_linear_fuses(x, dtype, ld_x, B, ldb, M, K))
         return status(mxq::launch_i8_linear_fused(x, dtype, ld_x, B, ldb, sB, bias, C, ldc, M, N, K, out_dtype,
                                                   hip(stream)));
     int8_t* q = static_cast<int8_t*>(workspace);
