@@ -438,19 +438,31 @@ __device__ void count_tiles(const int32_t* offs, int32_t G, int64_t M, uint32_t*
 }
 
 // The tile of this workgroup.  Workgroups are dealt to the 8 XCDs in turn, each
-// with its own L2.  Row groups: XCD x takes a contiguous eighth of the covered
+// with its own L2.  Dense: the tiles are numbered in bands of 8 row tiles,
+// column by column, and XCD x takes a contiguous eighth: a column's B is read
+// into one L2 (two at a seam), for all its row tiles at once.  (Dealt out
+// tile by tile every B was read into several L2s: [8192, 8192] by 128, 512 and
+// 1024 rows took 39.1, 74.0 and 80.1 us instead of 25.5, 42.4 and 66.8.)  Row groups: XCD x takes a contiguous eighth of the covered
 // row tiles, all column tiles of a row tile in a row, then its eighth of the
 // tail.
+constexpr uint32_t kBand = 8;
+
 template <int TM>
 __device__ bool place_tile(const I8Args& p, RowTile* r, uint32_t* tn) {
+    const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3;
     if (p.offs == nullptr) {
-        r->m0 = int64_t(blockIdx.x % p.tiles_m) * TM;
+        const uint32_t tiles = p.tiles_m * p.tiles_n;
+        const uint32_t lo = uint32_t(uint64_t(tiles) * xcd / 8u), hi = uint32_t(uint64_t(tiles) * (xcd + 1u) / 8u);
+        if (lo + j >= hi) return false;
+        const uint32_t band = (lo + j) / (kBand * p.tiles_n), in = lo + j - band * kBand * p.tiles_n;
+        const uint32_t height = min(kBand, p.tiles_m - band * kBand);
+        *tn = in / height;
+        r->m0 = int64_t(band * kBand + in - *tn * height) * TM;
         r->m1 = p.M;
         r->g = 0;
-        *tn = blockIdx.x / p.tiles_m;
         return true;
     }
-    const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3, lr = j / p.tiles_n;
+    const uint32_t lr = j / p.tiles_n;
     *tn = j - lr * p.tiles_n;
     uint32_t cov, all;
     count_tiles<TM>(p.offs, p.G, p.M, &cov, &all);
@@ -650,7 +662,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
 // operands at a time, and it waits for nothing but them, so up to kS steps of
 // every wave are under way at any moment and there is no barrier before the
 // sums meet.  (Fragments loaded into registers touch sixteen 64-byte pieces per
-// quarter wave instead, four times the cache lookups: RING.)
+// quarter wave instead, four times the cache lookups: one row through [8192, 8192]
+// takes 13.1 us here and 15.1 us so, 16 rows 13.7 and 20.8.)
 //
 // X != void: A is not codes but the activations themselves (float or bf16
 // bits): every workgroup quantizes the few rows into LDS, with its first
@@ -858,7 +871,7 @@ hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
     const int64_t tm = tile_bound(p.M, P::kTM, p.offs != nullptr, p.G);
     p.tiles_m = uint32_t(tm);
     p.tiles_n = uint32_t((p.N + P::kTN - 1) / P::kTN);
-    const uint32_t blocks = uint32_t(p.offs ? group_tiles(tm) : tm) * p.tiles_n;
+    const uint32_t blocks = p.offs ? uint32_t(group_tiles(tm)) * p.tiles_n : (uint32_t(tm) * p.tiles_n + 7u) / 8u * 8u;
     hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, ST, kStreamB>), dim3(blocks), dim3(64 * WM * WN), 0,
                        stream, p);
     return hipGetLastError();
@@ -915,10 +928,9 @@ struct Form {
 //
 // Dense: the piped tile with the least ceil(tiles / 256 CUs) (steps t + 1.2
 // us), t the time of one 128-code step: 256 x 256 1.25 us, 128 x 256 0.80,
-// 128 x 128 0.57, 128 x 64 0.51, 64 x 64 0.33.  These were fitted to all five
-// tiles' times over 39 shapes (M 32 to 4096; N, K 14336 x 4096, 8192 x 8192 and
-// 2048 x 5120), where the choice is 1.6% behind the best tile on average and
-// 28% at most.
+// 128 x 128 0.57, 128 x 64 0.51, 64 x 64 0.33.  With these the choice is the
+// fastest of the five tiles at each of the 42 shapes where all were timed (M
+// 32 to 8192; N, K 14336 x 4096, 8192 x 8192 and 2048 x 5120).
 Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) {
     auto stream = [&](int ms, int ns, int waves) {
         return Form{Kind::kStream, ms, ns,
@@ -927,7 +939,7 @@ Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) 
     const Form tiles{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
     auto piped = [&](int um, int un) {
         const int64_t tm = tile_bound(M, 64 * um, groups, G), tn = (N + 64 * un - 1) / (64 * un);
-        return Form{Kind::kPipe, um, un, uint64_t(groups ? group_tiles(tm) : tm) * uint64_t(tn) * 512};
+        return Form{Kind::kPipe, um, un, (groups ? uint64_t(group_tiles(tm)) * uint64_t(tn) : (uint64_t(tm) * uint64_t(tn) + 7) / 8 * 8) * 512};
     };
     if (groups) {
         const int64_t rows = (M + G - 1) / G;
