@@ -109,20 +109,36 @@ int64_t tile_bound(int64_t M, int64_t TM, bool groups, int32_t G) {
     return full + (parts < M ? parts : M);
 }
 
-// 16 codes of a row at k, zeros from K on; the row is any address.
-__device__ __forceinline__ v4i load_codes(const int8_t* row, int64_t k, int64_t K) {
-    v4i v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else if (k < K) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        const int n = int(K - k);
-#pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (i < n) w[i >> 2] |= uint32_t(uint8_t(row[k + i])) << (8 * (i & 3));
-        v = v4i{int(w[0]), int(w[1]), int(w[2]), int(w[3])};
-    }
+// 16 codes at any address (the hardware takes it whole; aligning it by hand
+// from whole dwords took up to twice the time of a product).
+__device__ __forceinline__ v4i load16(const int8_t* p) {
+    v4i v;
+    __builtin_memcpy(&v, p, 16);
     return v;
+}
+
+// 16 codes of a row at k, zeros from `end` on, where the row is K long (end <=
+// K): near the row's end its last 16 codes are read and shifted.
+__device__ __forceinline__ v4i load_codes(const int8_t* row, int64_t k, int64_t end, int64_t K) {
+    if (K < 16) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int i = 0; k + i < end; ++i) w[i >> 2] |= uint32_t(uint8_t(row[k + i])) << (8 * (i & 3));
+        return v4i{int(w[0]), int(w[1]), int(w[2]), int(w[3])};
+    }
+    const int64_t at = k + 16 <= K ? k : K - 16;
+    const v4i v = load16(row + at);
+    uint64_t lo = uint32_t(v[0]) | (uint64_t(uint32_t(v[1])) << 32), hi = uint32_t(v[2]) | (uint64_t(uint32_t(v[3])) << 32);
+    const int skip = int(k - at < 16 ? k - at : 16) * 8;                    // bits before k
+    if (skip >= 64) {
+        lo = skip < 128 ? hi >> (skip - 64) : 0;
+        hi = 0;
+    } else if (skip > 0) {
+        lo = (lo >> skip) | (hi << (64 - skip));
+        hi >>= skip;
+    }
+    const bool none = k >= end;                                             // `end` is K or whole pieces away
+    return none ? v4i{0, 0, 0, 0} : v4i{int(uint32_t(lo)), int(uint32_t(lo >> 32)), int(uint32_t(hi)), int(uint32_t(hi >> 32))};
 }
 
 template <typename O> struct Out;
@@ -175,8 +191,8 @@ __global__ __launch_bounds__(256, 2) void i8_gemm_kernel(I8Args p) {
         auto load = [&](int64_t k) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                va[i] = load_codes(ga[i], k + 16 * ch, p.K);
-                vb[i] = load_codes(gb[i], k + 16 * ch, p.K);
+                va[i] = k + 128 <= p.K ? load16(ga[i] + k + 16 * ch) : load_codes(ga[i], k + 16 * ch, p.K, p.K);
+                vb[i] = k + 128 <= p.K ? load16(gb[i] + k + 16 * ch) : load_codes(gb[i], k + 16 * ch, p.K, p.K);
             }
         };
         auto store = [&](int b) {
@@ -235,55 +251,82 @@ __global__ __launch_bounds__(256, 2) void i8_gemm_kernel(I8Args p) {
     }
 }
 
-// ---- few tiles: operands streamed from memory into the instructions ----
+// ---- few tiles, any alignment: every wave for itself ----
 //
-// One workgroup of kW waves computes (16 MS) x (16 NS) of C; its waves split
-// the contraction, each reading its own range of both operands straight into
-// fragments (no element is used by two waves, so LDS would only add a copy),
-// and their integer sums meet in LDS.  A lane's 16 bytes of 16 rows make 64
-// contiguous bytes of each row per load.  kU steps of 64 codes are loaded
-// before the first is multiplied.  With one to a few tokens this reads the
-// weights once at the rate of memory; with more it is used while whole tiles
-// would leave most CUs without work.
-__device__ __forceinline__ v4i load16(const int8_t* p) {
-    v4i v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
-}
+// One workgroup of kW waves computes (16 MS) x (16 NS) of C.  Wave w takes the
+// steps (128 codes) w, w + kW, ... of the contraction: it loads eight lanes to
+// a row, 16 bytes each, lays the pieces out in its own part of LDS (next
+// step's loads under way), and multiplies; the waves' integer sums meet at the
+// end.  (Loading fragments straight into registers, sixteen rows at a time,
+// touched four times as many cache lines per load: 77 x 1000 x 1111 took 8.8
+// us, 5.2 so.)
+// What a wave multiplies its share of a workgroup's sums by: accumulators
+// wave, wave + kW, ... of the (16 MS) x (16 NS) tile.  Read before the
+// contraction, whose loads hide theirs.
+template <int MS, int NS, int kW>
+struct Share {
+    static constexpr int kRegs = MS * NS * 4, kN = (kRegs + kW - 1) / kW;
+    float sa[kN], sb[kN], bias[kN];
+
+    static __device__ __forceinline__ void place(uint32_t q, const RowTile& r, int64_t n0, int64_t* row, int64_t* col) {
+        const uint32_t lane = threadIdx.x & 63u, i = q / (4 * NS), j = q / 4 % NS, v = q & 3u;
+        *row = r.m0 + 16 * i + 4 * (lane >> 4) + v;
+        *col = n0 + 16 * j + (lane & 15u);
+    }
+    __device__ __forceinline__ void load(const I8Args& p, const RowTile& r, int64_t n0, uint32_t wave, const float* sA,
+                                         const float* sB) {
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            int64_t row, col;
+            place(wave + kW * x, r, n0, &row, &col);
+            row = row < r.m1 ? row : r.m1 - 1;
+            col = col < p.N ? col : p.N - 1;
+            sa[x] = sA ? sA[row] : 0.f;
+            sb[x] = sB[col];
+            bias[x] = p.bias ? p.bias[col] : 0.f;
+        }
+    }
+};
 
 // The sums of a workgroup's waves, which split the contraction, meet in LDS
-// and become C's (16 MS) x (16 NS) tile.
+// and become C's tile.  sA: in LDS, or null where the share has them.
 template <typename O, int MS, int NS, int kW>
 __device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[MS][NS], int* sums, const RowTile& r,
-                                           int64_t n0, const float* sB, const float* sA, bool zero) {
-    constexpr int kRegs = MS * NS * 4;
-    const uint32_t t = threadIdx.x, lane = t & 63u, wave = uint32_t(uniform(int32_t(t >> 6)));
+                                           int64_t n0, uint32_t wave, const Share<MS, NS, kW>& share, const float* sA,
+                                           bool zero) {
+    using S = Share<MS, NS, kW>;
+    const uint32_t lane = threadIdx.x & 63u;
 #pragma unroll
     for (int i = 0; i < MS; ++i)
 #pragma unroll
         for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sums[(wave * kRegs + (i * NS + j) * 4 + v) * 64 + lane] = acc[i][j][v];
+            for (int v = 0; v < 4; ++v) sums[(wave * S::kRegs + (i * NS + j) * 4 + v) * 64 + lane] = acc[i][j][v];
     __syncthreads();
     O* C = static_cast<O*>(p.C);
-    for (uint32_t q = wave; q < uint32_t(kRegs); q += kW) {
+#pragma unroll
+    for (int x = 0; x < S::kN; ++x) {
+        const uint32_t q = wave + kW * x;
+        if (q >= uint32_t(S::kRegs)) break;                                 // uniform
         int sum = 0;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) sum += sums[(w * kRegs + q) * 64 + lane];
-        const uint32_t i = q / (4 * NS), j = q / 4 % NS, v = q & 3u;
-        const int64_t row = r.m0 + 16 * i + 4 * (lane >> 4) + v, col = n0 + 16 * j + (lane & 15u);
+        for (int w = 0; w < kW; ++w) sum += sums[(w * S::kRegs + q) * 64 + lane];
+        int64_t row, col;
+        S::place(q, r, n0, &row, &col);
         if (row >= r.m1 || col >= p.N) continue;
-        float x = float(sum) * sA[row];
-        x = p.bias ? __builtin_fmaf(x, sB[col], p.bias[col]) : x * sB[col];
-        C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : x);
+        float y = float(sum) * (sA ? sA[row] : share.sa[x]);
+        y = p.bias ? __builtin_fmaf(y, share.sb[x], share.bias[x]) : y * share.sb[x];
+        C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : y);
     }
 }
 
-template <typename O, int MS, int NS, int kW, int kU>
-__global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
-    __shared__ __attribute__((aligned(16))) int sums[kW * MS * NS * 4 * 64];
-    const uint32_t t = threadIdx.x, lane = t & 63u, l16 = lane & 15u, g = lane >> 4;
-    const uint32_t wave = uint32_t(uniform(int32_t(t >> 6)));
+template <typename O, int MS, int NS, int kW>
+__global__ __launch_bounds__(64 * kW) void i8_split_kernel(I8Args p) {
+    constexpr int kRows = 16 * (MS + NS), kLA = 2 * MS, kL = 2 * (MS + NS);
+    static_assert(kRows * 8 * 4 >= MS * NS * 4 * 64, "the sums take a wave's part of LDS");
+    __shared__ v4i lds[kW * kRows * 8];
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = uint32_t(uniform(int32_t(threadIdx.x >> 6)));
     const uint32_t tm = p.offs ? blockIdx.x / p.tiles_n : blockIdx.x % p.tiles_m;
     const uint32_t tn = p.offs ? blockIdx.x - tm * p.tiles_n : blockIdx.x / p.tiles_m;
     RowTile r;
@@ -292,59 +335,59 @@ __global__ __launch_bounds__(64 * kW) void i8_stream_kernel(I8Args p) {
     const bool zero = p.offs != nullptr && r.g >= p.G;
     const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs);
     const float* sB = p.sB + (zero ? 0 : int64_t(r.g) * p.sb_gs);
+    Share<MS, NS, kW> share;
+    share.load(p, r, n0, wave, p.sA, sB);
 
-    const int64_t per = (p.K + kW * 128 - 1) / (kW * 128) * 128;
-    const int64_t k0 = zero ? p.K : min(int64_t(wave) * per, p.K), k1 = min(k0 + per, p.K);
-    const int8_t *pa[MS], *pb[NS];
+    // load q brings rows 8 q .. 8 q + 7 of A's tile, then of B's; rows past the end repeat the last
+    const uint32_t lr = lane >> 3, piece = lane & 7u;
+    const int8_t* from[kL];
 #pragma unroll
-    for (int i = 0; i < MS; ++i) {
-        const int64_t row = r.m0 + 16 * i + l16;
-        pa[i] = p.A + (row < r.m1 ? row : r.m1 - 1) * p.lda + 16 * g;
+    for (int q = 0; q < kL; ++q) {
+        const int64_t ar = r.m0 + 8 * q + lr, br = n0 + 8 * (q - kLA) + lr;
+        from[q] = q < kLA ? p.A + (ar < r.m1 ? ar : r.m1 - 1) * p.lda : B + (br < p.N ? br : p.N - 1) * p.ldb;
     }
+    v4i* part = lds + wave * (kRows * 8);
+    const uint32_t at = lr * 8u + (piece ^ lr);
+    v4i v[kL];
+    auto load = [&](int64_t k) {
+        if (k + 128 <= p.K) {                                              // uniform
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int64_t row = n0 + 16 * j + l16;
-        pb[j] = B + (row < p.N ? row : p.N - 1) * p.ldb + 16 * g;
-    }
+            for (int q = 0; q < kL; ++q) v[q] = load16(from[q] + k + 16 * piece);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kL; ++q) v[q] = load_codes(from[q], k + 16 * piece, p.K, p.K);
+        }
+    };
     v4i acc[MS][NS];
 #pragma unroll
     for (int i = 0; i < MS; ++i)
 #pragma unroll
         for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-
-    int64_t k = k0;
-    for (; k + 64 * kU <= k1; k += 64 * kU) {
-        v4i b[kU][NS];
+    int64_t k = zero ? p.K : 128 * int64_t(wave);
+    if (k < p.K) load(k);
+    for (; k < p.K; k += 128 * kW) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+        for (int q = 0; q < kL; ++q) part[64 * q + at] = v[q];
+        if (k + 128 * kW < p.K) load(k + 128 * kW);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-            for (int j = 0; j < NS; ++j) b[u][j] = load16(pb[j] + k + 64 * u);
-        v4i a[kU][MS];
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = (4u * h + g) ^ (l16 & 7u);
+            v4i a[MS], b[NS];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+            for (int i = 0; i < MS; ++i) a[i] = part[(16u * i + l16) * 8u + c];
 #pragma unroll
-            for (int i = 0; i < MS; ++i) a[u][i] = load16(pa[i] + k + 64 * u);
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
+            for (int j = 0; j < NS; ++j) b[j] = part[(16u * (MS + j) + l16) * 8u + c];
 #pragma unroll
             for (int i = 0; i < MS; ++i)
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][i], b[u][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    for (; k < k1; k += 64) {
-        v4i a[MS], c[NS];
-#pragma unroll
-        for (int i = 0; i < MS; ++i) a[i] = load_codes(pa[i] - 16 * g, k + 16 * g, p.K);
-#pragma unroll
-        for (int j = 0; j < NS; ++j) c[j] = load_codes(pb[j] - 16 * g, k + 16 * g, p.K);
-#pragma unroll
-        for (int i = 0; i < MS; ++i)
-#pragma unroll
-            for (int j = 0; j < NS; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], c[j], acc[i][j], 0, 0, 0);
-    }
-
-    store_sums<O, MS, NS, kW>(p, acc, sums, r, n0, sB, p.sA, zero);
+    __syncthreads();                                                       // every part is read
+    store_sums<O, MS, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, nullptr, zero);
 }
 
 // ---- many tiles, aligned operands: pipelined through LDS ----
@@ -806,6 +849,8 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
         for (uint32_t i = 0; i < uint32_t(kS); ++i)
             if (i < mine) issue(i, i);
     };
+    Share<1, NS, kW> share;
+    share.load(p, r, n0, wave, kFuse ? nullptr : p.sA, p.sB);
     const uint32_t pitch = (K + 127u) / 128u * 128u + 16u;
     uint8_t* codes = lds + kRing;
     if constexpr (kFuse) {
@@ -851,7 +896,7 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
         slot = slot + 1u == uint32_t(kS) ? 0u : slot + 1u;
     }
     __syncthreads();                                                         // every ring is read
-    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, p.sB, kFuse ? scales : p.sA, false);
+    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, kFuse ? scales : nullptr, false);
 }
 
 template <typename O, int NS, int kW, int kS, typename X>
@@ -877,11 +922,12 @@ hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename O, int MS, int NS, int kW, int kU>
-hipError_t launch_stream(I8Args& p, hipStream_t stream) {
+template <typename O, int MS, int NS, int kW>
+hipError_t launch_split(I8Args& p, hipStream_t stream) {
     p.tiles_m = uint32_t(tile_bound(p.M, 16 * MS, p.offs != nullptr, p.G));
     p.tiles_n = uint32_t((p.N + 16 * NS - 1) / (16 * NS));
-    hipLaunchKernelGGL((i8_stream_kernel<O, MS, NS, kW, kU>), dim3(p.tiles_m * p.tiles_n), dim3(64 * kW), 0, stream, p);
+    const dim3 grid(p.tiles_m * p.tiles_n), block(64 * kW);
+    hipLaunchKernelGGL((i8_split_kernel<O, MS, NS, kW>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -889,7 +935,8 @@ template <typename O>
 hipError_t launch_tiles(I8Args& p, hipStream_t stream) {
     p.tiles_m = uint32_t(tile_bound(p.M, kTile, p.offs != nullptr, p.G));
     p.tiles_n = uint32_t((p.N + kTile - 1) / kTile);
-    hipLaunchKernelGGL(i8_gemm_kernel<O>, dim3(p.tiles_m * p.tiles_n), dim3(256), 0, stream, p);
+    const dim3 grid(p.tiles_m * p.tiles_n), block(256);
+    hipLaunchKernelGGL(i8_gemm_kernel<O>, grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -908,23 +955,22 @@ hipError_t ring(I8Args& p, hipStream_t stream) {
 }
 
 // Which kernel.
-enum class Kind { kStream, kTiles, kRing, kPipe };
+enum class Kind { kSplit, kTiles, kRing, kPipe };
 struct Form {
     Kind kind;
-    int ms, ns;                  // kStream: 16-row, 16-column sub-tiles of a workgroup; kPipe: 64-row, 64-column units
+    int ms, ns;                  // kSplit: 16-row, 16-column sub-tiles of a workgroup; kPipe: 64-row, 64-column units
     uint64_t threads;            // of the grid
 };
 
 // pipe: the operands are whole aligned 16-byte pieces.
 //
 // Row groups, by the mean rows of a group (64 experts of [2048, 5120], group
-// sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows, and streamed):
-//   rows    4: 108.0  117.6           145.5       rows  48: 141.8  147.3  156.3  266.1
-//   rows   16: 107.6  113.9           186.6       rows 128: 234.1  173.5  201.1
-//   rows   24: 134.7  113.1  159.4    204.1       rows 192:        229.1  214.0
-//   rows   32: 135.3  115.0  153.9    217.3       rows 384:        394.6  320.1
-// (the 671 MB of weights alone take 108 us at 6.2 TB/s).  Groups of unaligned
-// operands are streamed while they are small.
+// sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows):
+//   rows   4: 108.0  117.6         rows  48: 141.8  147.3  156.3
+//   rows  16: 107.6  113.9         rows 128: 234.1  173.5  201.1
+//   rows  24: 134.7  113.1  159.4  rows 192:        229.1  214.0
+//   rows  32: 135.3  115.0  153.9  rows 384:        394.6  320.1
+// (the 671 MB of weights alone take 108 us at 6.2 TB/s).
 //
 // Dense: the piped tile with the least ceil(tiles / 256 CUs) (steps t + 1.2
 // us), t the time of one 128-code step: 256 x 256 1.25 us, 128 x 256 0.80,
@@ -932,8 +978,8 @@ struct Form {
 // fastest of the five tiles at each of the 42 shapes where all were timed (M
 // 32 to 8192; N, K 14336 x 4096, 8192 x 8192 and 2048 x 5120).
 Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) {
-    auto stream = [&](int ms, int ns, int waves) {
-        return Form{Kind::kStream, ms, ns,
+    auto split = [&](int ms, int ns, int waves) {
+        return Form{Kind::kSplit, ms, ns,
                     uint64_t(tile_bound(M, 16 * ms, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 64u * uint64_t(waves)};
     };
     const Form tiles{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
@@ -944,10 +990,10 @@ Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) 
     if (groups) {
         const int64_t rows = (M + G - 1) / G;
         if (pipe) return piped(rows <= 16 ? 1 : rows <= 160 ? 2 : 4, 4);
-        if (rows <= 8) return stream(1, 2, 8);
-        if (rows <= 20) return stream(2, 2, 8);
-        if (rows <= 48) return stream(4, 2, 8);
-        return tiles;
+        // rows that start at any byte, 64 of [2047, 5119] by 1, 8, 16, 24, 60 rows a
+        // group: 16 x 32 split 150, 186, 223, 267, 495 us, 128 x 128 tiles 225, 237,
+        // 239, 239, 317
+        return rows <= 18 ? split(1, 2, 8) : tiles;
     }
     if (pipe) {
         if (M <= 16) return Form{Kind::kRing, 1, ring_columns(N), uint64_t((N + 15) / 16) * 512};
@@ -968,9 +1014,11 @@ Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) 
         }
         return piped(best->um, best->un);
     }
-    if (M <= 16) return N >= 16384 ? stream(1, 2, 8) : stream(1, 1, 8);
-    if (((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) >= 192) return tiles;
-    return ((M + 63) / 64) * ((N + 63) / 64) >= 192 ? stream(4, 4, 4) : stream(2, 2, 8);
+    // rows that start at any byte, [8191, 4095] by 16, 64, 256, 512 rows: 16 x 16
+    // split 14.0, 35.2, 111.8, 209.9 us, 64 x 32 split 21.2, 21.5, 58.0, 102.9, 128 x
+    // 128 tiles 65.2, 70.2, 70.4, 70.7
+    if (((M + 15) / 16) * ((N + 15) / 16) <= 1024) return split(1, 1, 8);
+    return ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) < 192 ? split(4, 2, 4) : tiles;
 }
 
 bool pipe_fits(const I8Args& p) {
@@ -1000,11 +1048,9 @@ hipError_t launch(I8Args& p, hipStream_t stream) {
     }
     if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
     switch (f.ms * 8 + f.ns) {
-        case 8 + 1: return launch_stream<O, 1, 1, 8, 8>(p, stream);
-        case 8 + 2: return launch_stream<O, 1, 2, 8, 4>(p, stream);
-        case 16 + 2: return launch_stream<O, 2, 2, 8, 4>(p, stream);
-        case 32 + 2: return launch_stream<O, 4, 2, 8, 2>(p, stream);
-        default: return launch_stream<O, 4, 4, 4, 2>(p, stream);
+        case 8 + 1: return launch_split<O, 1, 1, 8>(p, stream);
+        case 8 + 2: return launch_split<O, 1, 2, 8>(p, stream);
+        default: return launch_split<O, 4, 2, 4>(p, stream);
     }
 }
 

@@ -92,6 +92,16 @@ __device__ __forceinline__ void zero_row(char* p, int64_t bytes, int esz, uint32
     }
 }
 
+constexpr int kMaxPicks = 64;
+
+// Which of the kPadRows rows from r0 belong to no token: one load, one bit each.
+__device__ __forceinline__ uint32_t pad_rows(const int32_t* src, int64_t r0, int64_t M) {
+    const uint32_t lane = threadIdx.x & 63u;
+    bool pad = false;
+    if (lane < kPadRows && r0 + lane < M) pad = src[r0 + lane] < 0;
+    return uint32_t(__ballot(pad));
+}
+
 // ------------------------------------------------------------------ dispatch
 struct DispatchArgs {
     const char* x;
@@ -145,14 +155,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs p) {
     const int64_t u = w - tokens, g = u / p.chunks, c0 = (u - g * p.chunks) * kChunk;
     const int64_t r0 = g * kPadRows;
     if (r0 >= p.M) return;
-    bool pad = false;
-    if (lane < kPadRows && r0 + lane < p.M) pad = p.src[r0 + lane] < 0;
-    uint64_t rows = __ballot(pad);
+    uint32_t rows = pad_rows(p.src, r0, p.M);
     const int64_t n = p.row - c0 < kChunk ? p.row - c0 : kChunk;
     // a last chunk shorter than a piece is zeroed with the piece before it
     const int64_t from = n < 16 && c0 > 0 ? c0 - 16 : c0;
     while (rows) {
-        const int r = __builtin_ctzll(rows);
+        const int r = __builtin_ctz(rows);
         rows &= rows - 1;
         zero_row(p.out + (r0 + r) * p.ld_out + from, n + (c0 - from), p.esz, lane, 64);
     }
@@ -184,17 +192,23 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
     constexpr int kPer = Elem<T>::kPer, kHold = 4;
     constexpr float kFloor = 127.f * 0x1p-126f;
     __shared__ uint32_t sh[4];
+    __shared__ int32_t rows[kMaxPicks];                                     // where this token's codes go, or -1
     const uint32_t t = threadIdx.x;
     if (int64_t(blockIdx.x) >= p.T) {
         const int64_t r0 = (int64_t(blockIdx.x) - p.T) * kPadRows;
-        for (int64_t r = r0; r < r0 + kPadRows && r < p.M; ++r) {
-            if (p.src[r] >= 0) continue;
+        for (uint32_t pads = pad_rows(p.src, r0, p.M); pads != 0; pads &= pads - 1) {
+            const int64_t r = r0 + __builtin_ctz(pads);
             zero_row(reinterpret_cast<char*>(p.q) + r * p.ld_q, p.K, 1, t, kThreads);
             if (t == 0) p.s[r] = kFloor / 127.f;
         }
         return;
     }
     const int64_t tok = blockIdx.x;
+    const int32_t n = p.slot ? p.k : 1;
+    if (t < uint32_t(n)) {
+        const int64_t r = p.slot ? int64_t(p.slot[tok * n + t]) : tok;
+        rows[t] = r >= 0 && r < p.M ? int32_t(r) : -1;
+    }
     const char* x = p.x + tok * p.ld_x;
     const int64_t bytes = p.K * int64_t(sizeof(T));
     const bool whole = bytes >= 16;
@@ -233,11 +247,6 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
     const float inv = bad ? 0.f : 127.f / a;
     const float s = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
 
-    const int32_t n = p.slot ? p.k : 1;
-    auto row_of = [&](int32_t j) -> int64_t {
-        const int64_t r = p.slot ? int64_t(p.slot[tok * p.k + j]) : tok;
-        return r >= 0 && r < p.M ? r : -1;
-    };
     auto put = [&](int64_t c, u32x4 v) {
         float f[kPer];
         Elem<T>::get(v, f);
@@ -249,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
         }
         const int64_t at = c * kPer + kPer > p.K ? p.K - kPer : c * kPer;
         for (int32_t j = 0; j < n; ++j) {
-            const int64_t r = row_of(j);
+            const int64_t r = rows[j];
             if (r >= 0) __builtin_memcpy(p.q + r * p.ld_q + at, o, kPer);
         }
     };
@@ -261,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
     for (int64_t c = int64_t(kHold) * kThreads + t; c < pieces; c += kThreads)
         put(c, load16(x + (16 * c + 16 > bytes ? bytes - 16 : 16 * c)));
     for (int32_t j = 0; j < n; ++j) {
-        const int64_t r = row_of(j);
+        const int64_t r = rows[j];
         if (r < 0) continue;
         if (!whole && int64_t(t) < p.K) p.q[r * p.ld_q + t] = bad ? int8_t(0) : int8_t(int(rintf(lone * inv)));
         if (t == 0) p.s[r] = s;
@@ -334,8 +343,6 @@ struct CombineGradArgs {
     float* dweight;
 };
 
-constexpr int kMaxPicks = 64;
-
 // One block per token: dy stays in registers over the token's rows.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs p) {
@@ -345,8 +352,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
     const int64_t bytes = p.N * int64_t(sizeof(T));
     if (int64_t(blockIdx.x) >= p.T) {
         const int64_t r0 = (int64_t(blockIdx.x) - p.T) * kPadRows;
-        for (int64_t r = r0; r < r0 + kPadRows && r < p.M; ++r)
-            if (p.src[r] < 0) zero_row(p.drows + r * p.ld_d, bytes, int(sizeof(T)), t, kThreads);
+        for (uint32_t pads = pad_rows(p.src, r0, p.M); pads != 0; pads &= pads - 1)
+            zero_row(p.drows + (r0 + __builtin_ctz(pads)) * p.ld_d, bytes, int(sizeof(T)), t, kThreads);
         return;
     }
     const int64_t tok = blockIdx.x;
