@@ -63,22 +63,42 @@ def _L():
     return _lib
 
 
+_device = torch._C._cuda_getDevice
+_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _run(dev, f, *args):
     """Call an entry point on `dev`'s current stream and raise on a status."""
     i = dev.index
-    if i == torch._C._cuda_getDevice():
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if i == _device():
+        rc = f(*args, _stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+            rc = f(*args, _stream(i))
     if rc:
         from . import MXError, status_string
 
         raise MXError(rc, status_string(rc))
 
 
+# The checks below answer for a good argument at once; what is wrong with a bad
+# one is found out apart, since the smallest calls last as long as their checks.
 def _matrix(t, name, dtypes, dev=None):
     """A 2-d device tensor with contiguous rows; returns its row pitch."""
+    try:
+        rows, cols = t.shape
+        pitch, step = t.stride()
+        if t.is_cuda and t.dtype in dtypes and (step == 1 or cols <= 1) and (dev is None or t.device == dev):
+            if pitch >= cols:
+                return pitch
+            if rows <= 1:
+                return cols
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _bad_matrix(t, name, dtypes, dev)
+
+
+def _bad_matrix(t, name, dtypes, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype not in dtypes:
@@ -87,26 +107,21 @@ def _matrix(t, name, dtypes, dev=None):
         raise ValueError(f"{name} must have two dimensions, not {tuple(t.shape)}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
-    rows, cols = t.shape
-    pitch, step = t.stride()
-    if step != 1 and cols > 1:
+    if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1:
-        return max(pitch, cols)
-    if pitch < cols:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return pitch
+    raise ValueError(f"the rows of {name} must not overlap")
 
 
 def _flat(t, name, dtype, shape, dev):
     """A contiguous device tensor of one dtype and shape; returns its pointer."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+            return t.data_ptr()
+        if t.dtype is dtype and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+        if t.dtype is dtype:
+            raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a {dtype} tensor")
 
 
 def _valid(valid, T, dev):
@@ -117,10 +132,11 @@ def _valid(valid, T, dev):
     return _flat(valid, "valid", torch.uint8, (T,), dev)
 
 
-def _out_matrix(out, name, shape, dtype, dev):
+def _out_matrix(out, name, shape, dtype, like):
+    """`out`, or a new matrix on the device of `like`; and its row pitch."""
+    dev = like.device
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-        return out, shape[1]
+        return like.new_empty(shape, dtype=dtype), shape[1]
     pitch = _matrix(out, name, (dtype,), dev)
     if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(out.shape)}")
@@ -204,7 +220,7 @@ def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tenso
         raise ValueError("routing was made for other logits")
     dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), dev)
     dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), dev)
-    out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, dev)
+    out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, logits)
     p = routing._ptrs
     _run(dev, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, dev), routing.k,
          1 if routing.normalize else 0, p[0], p[1], dw, p[4], p[6], dl, out.data_ptr(), ld_d)
@@ -214,15 +230,15 @@ def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tenso
 def _slots(slot, dev):
     if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
         raise ValueError("slot must be an int32 [T, k] tensor")
-    T, k = slot.shape
-    return _flat(slot, "slot", _I32, (T, k), dev), T, k
+    shape = slot.shape
+    return _flat(slot, "slot", _I32, shape, dev), shape[0], shape[1]
 
 
 def _src(src, dev):
     if not isinstance(src, torch.Tensor) or src.dim() != 1:
         raise ValueError("src must be an int32 [M] tensor")
-    M = src.shape[0]
-    return _flat(src, "src", _I32, (M,), dev), M
+    shape = src.shape
+    return _flat(src, "src", _I32, shape, dev), shape[0]
 
 
 def mx_dispatch(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out: torch.Tensor | None = None):
@@ -235,21 +251,23 @@ def mx_dispatch(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out: tor
     if T != x.shape[0]:
         raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
     N = x.shape[1]
-    out, ld_o = _out_matrix(out, "out", (M, N), x.dtype, dev)
+    out, ld_o = _out_matrix(out, "out", (M, N), x.dtype, x)
     _run(dev, _L().mx_dispatch, x.data_ptr(), _ESZ[x.dtype], T, N, ld, sp, rp, k, M, out.data_ptr(), ld_o)
     return out
 
 
-def _codes_out(out, rows, K, dev):
+def _codes_out(out, rows, K, like):
     """(q, its pitch, s): new codes get rows of whole 16-byte pieces, which the
     products read fastest."""
     if out is None:
         pitch = (K + 15) // 16 * 16
-        q = torch.empty((rows, pitch), dtype=_I8, device=dev)
-        return (q if pitch == K else q[:, :K]), pitch, torch.empty((rows,), dtype=_F32, device=dev)
+        q = like.new_empty((rows, pitch), dtype=_I8)
+        return (q if pitch == K else q[:, :K]), pitch, like.new_empty((rows,), dtype=_F32)
     q, s = out
-    q, pitch = _out_matrix(q, "out[0]", (rows, K), _I8, dev)
-    _flat(s, "out[1]", _F32, (rows,), dev)
+    if q is None:
+        raise ValueError("out must be two tensors, the codes and the scales")
+    q, pitch = _out_matrix(q, "out[0]", (rows, K), _I8, like)
+    _flat(s, "out[1]", _F32, (rows,), like.device)
     return q, pitch, s
 
 
@@ -262,7 +280,7 @@ def mx_dispatch_i8(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out=N
     if T != x.shape[0]:
         raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
     K = x.shape[1]
-    q, pitch, s = _codes_out(out, M, K, dev)
+    q, pitch, s = _codes_out(out, M, K, x)
     _run(dev, _L().mx_dispatch_i8, x.data_ptr(), _ESZ[x.dtype], T, K, ld, sp, rp, k, M, q.data_ptr(), pitch,
          s.data_ptr())
     return q, s
@@ -272,7 +290,7 @@ def i8_quantize_rows(x: torch.Tensor, out=None):
     """(q int8 [T, K], s float32 [T]): x[t] ~ q[t] s[t], s = max |x[t]| / 127."""
     ld = _matrix(x, "x", _ESZ)
     T, K = x.shape
-    q, pitch, s = _codes_out(out, T, K, x.device)
+    q, pitch, s = _codes_out(out, T, K, x)
     _run(x.device, _L().i8_quantize_rows, x.data_ptr(), _ESZ[x.dtype], T, K, ld, q.data_ptr(), pitch, s.data_ptr())
     return q, s
 
@@ -281,14 +299,14 @@ def _bias(bias, N, dev):
     return None if bias is None else _flat(bias, "bias", _F32, (N,), dev)
 
 
-def _product_out(out, shape, out_dtype, dev):
+def _product_out(out, shape, out_dtype, like):
     if out is None:
         if out_dtype not in _ESZ:
             raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
-        return torch.empty(shape, dtype=out_dtype, device=dev), shape[1]
+        return like.new_empty(shape, dtype=out_dtype), shape[1]
     if out.dtype not in _ESZ:
         raise ValueError(f"out must be float32 or bfloat16, not {out.dtype}")
-    return _out_matrix(out, "out", shape, out.dtype, dev)
+    return _out_matrix(out, "out", shape, out.dtype, like)
 
 
 def i8_gemm_nt(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
@@ -303,7 +321,7 @@ def i8_gemm_nt(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Ten
     if B.shape[1] != K:
         raise ValueError("A and B must share the contraction extent")
     sa, sb, bi = _flat(sA, "sA", _F32, (M,), dev), _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
-    out, ldc = _product_out(out, (M, N), out_dtype, dev)
+    out, ldc = _product_out(out, (M, N), out_dtype, A)
     _run(dev, _L().i8_gemm_nt, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
          _ESZ[out.dtype])
     return out
@@ -321,9 +339,9 @@ def i8_linear(x: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, bias: torch.Te
     if B.shape[1] != K:
         raise ValueError("x and B must share the contraction extent")
     sb, bi = _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
-    out, ldc = _product_out(out, (M, N), out_dtype or x.dtype, dev)
+    out, ldc = _product_out(out, (M, N), out_dtype or x.dtype, x)
     size = M * ((K + 15) // 16 * 16) + (M * 4 + 15) // 16 * 16
-    ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+    ws = x.new_empty((size,), dtype=torch.uint8)
     _run(dev, _L().i8_linear, x.data_ptr(), _ESZ[x.dtype], ld, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
          _ESZ[out.dtype], ws.data_ptr(), size)
     return out
@@ -349,7 +367,7 @@ def i8_grouped_gemm_rows(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB:
         raise ValueError("offs must be an int32 [G] tensor with 1 <= G <= E")
     G = offs.shape[0]
     sa, of = _flat(sA, "sA", _F32, (M,), dev), _flat(offs, "offs", _I32, (G,), dev)
-    out, ldc = _product_out(out, (M, N), out_dtype, dev)
+    out, ldc = _product_out(out, (M, N), out_dtype, A)
     _run(dev, _L().i8_grouped_gemm_rows, A.data_ptr(), lda, sa, B.data_ptr(), max(B.stride(1), K), B.stride(0),
          sB.data_ptr(), sB.stride(0), of, G, M, N, K, out.data_ptr(), ldc, _ESZ[out.dtype])
     return out
@@ -364,7 +382,7 @@ def mx_combine(rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor | No
     sp, T, k = _slots(slot, dev)
     wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
     M, N = rows.shape
-    out, ld_y = _out_matrix(out, "out", (T, N), rows.dtype, dev)
+    out, ld_y = _out_matrix(out, "out", (T, N), rows.dtype, rows)
     _run(dev, _L().mx_combine, rows.data_ptr(), _ESZ[rows.dtype], M, N, ld, sp, wp, k, T, out.data_ptr(), ld_y)
     return out
 
@@ -384,9 +402,9 @@ def mx_combine_grad(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, we
         raise ValueError(f"dy must be [{T}, N] and rows [{M}, N], not {tuple(dy.shape)} and {tuple(rows.shape)}")
     wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
     drows, dweight = out if out is not None else (None, None)
-    drows, ld_d = _out_matrix(drows, "out[0]", (M, N), dy.dtype, dev)
+    drows, ld_d = _out_matrix(drows, "out[0]", (M, N), dy.dtype, dy)
     if dweight is None:
-        dweight = torch.empty((T, k), dtype=_F32, device=dev)
+        dweight = dy.new_empty((T, k), dtype=_F32)
     dp = _flat(dweight, "out[1]", _F32, (T, k), dev)
     _run(dev, _L().mx_combine_grad, dy.data_ptr(), _ESZ[dy.dtype], T, N, ld_g, rows.data_ptr(), ld_r, sp, wp, rp, k, M,
          drows.data_ptr(), ld_d, dp)
