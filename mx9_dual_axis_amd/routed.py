@@ -148,10 +148,17 @@ class MXRouting:
     call to call; made by mx_routing.
 
     idx, weight, slot [T, k]; src [rows]; counts, offs, prob [E]; live, loss
-    [1]: see mx_route.  `normalize` is what the last mx_route used."""
+    [1]: see mx_route.  `normalize` is what the last mx_route used.  The
+    tensors stay the plan's own: none can be put in another's place, and none
+    may be resized."""
 
     __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "idx", "weight", "slot", "src", "counts",
                  "offs", "live", "prob", "loss", "_workspace", "_ptrs")
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_ptrs") and name != "normalize":
+            raise AttributeError(f"{name} of a routing cannot be replaced")
+        object.__setattr__(self, name, value)
 
     def __init__(self, T, E, k, align, device):
         lib = _L()
