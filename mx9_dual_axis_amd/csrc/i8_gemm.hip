@@ -20,6 +20,8 @@
 // 64 group ends at a time.
 #include "mxq_kernels.h"
 
+#include <type_traits>
+
 namespace mxq {
 namespace {
 
@@ -392,11 +394,17 @@ __global__ __launch_bounds__(64 * kW) void i8_split_kernel(I8Args p) {
 
 // ---- many tiles, aligned operands: pipelined through LDS ----
 //
-// WM x WN waves, each (16 MS) x (16 NS) of the tile.  A stage holds 128 codes
-// of every row of both operands; buffer loads put 16-byte pieces from memory
-// straight into LDS (no registers stage them), the swizzle applied to the
-// address they read, and run kStages - 1 steps ahead.  Loads complete in
-// order, so a step waits only until the later steps' loads are the ones
+// WM x WN waves, each MS x NS fragments of 16 x 16.  A wave's row fragments lie
+// 16 WM apart, so that every wave has its part of a tile of few rows, and
+// groups multiply only the fragments that hold rows (64 experts of [2048, 5120],
+// mean rows 64 and 128: 151 and 164 us so, 169 and 171 with whole tiles).  A
+// stage holds 128 codes of every row of an operand; buffer loads put 16-byte
+// pieces from memory straight into LDS (no registers stage them), the swizzle
+// applied to the address they read, and run SA - 1 (A) and SB - 1 (B) steps
+// ahead.  Experts' B comes from HBM, A mostly from L2, so there B runs further
+// ahead (mean rows 384 and 512: 2 and 3 stages 317 and 411 us, 2 and 2 325 and
+// 433); dense operands, both from L2, gain nothing by it.  Loads complete in
+// order, so a step waits only until what was issued after its own is what is
 // outstanding; wait and barrier are one asm block, because the compiler's
 // barrier would wait for every load.  Within a step a wave keeps all its A
 // fragments and reads B one column ahead of the instructions.
@@ -430,18 +438,18 @@ __device__ __forceinline__ void pipe_sync() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-template <int MS, int NS, int WM, int WN, int ST>
+template <int MS, int NS, int WM, int WN, int SA, int SB>
 struct Pipe {
-    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int kWM = WM, kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int kTM = 16 * MS * WM, kTN = 16 * NS * WN;
     static constexpr int kLA = kTM / 8 / kWaves, kLB = kTN / 8 / kWaves;    // loads per wave and step
-    static constexpr uint32_t kB = uint32_t(kTM) * 128, kStage = kB + uint32_t(kTN) * 128;
-    static constexpr int kStages = ST;
-    static constexpr uint32_t kScales = kStages * kStage;                   // sA, sB, bias of the tile
-    static constexpr uint32_t kLds = kScales + uint32_t(kTM + 2 * kTN) * 4;
-    static constexpr int kLoads = kLA + kLB;
+    static constexpr uint32_t kStageA = uint32_t(kTM) * 128, kStageB = uint32_t(kTN) * 128;
+    static constexpr uint32_t kB = SA * kStageA, kLds = kB + SB * kStageB;  // B's stages follow A's
+    static constexpr uint32_t kScales = kLds - uint32_t(kTM + 2 * kTN) * 4; // sA, sB, bias of the tile, once the stages are free
+    // loads that may be outstanding while a step's own have arrived
+    static constexpr int kLater = (SA - 2) * (kLA + kLB) + (SB > SA ? kLB : 0);
     static_assert(kLA * kWaves * 8 == kTM && kLB * kWaves * 8 == kTN && kLds <= 160 * 1024, "tile");
-    static_assert(kThreads >= kTM && kThreads >= kTN && (kStages - 2) * kLoads < 64, "scales: one per thread; vmcnt");
+    static_assert(kThreads >= kTM && kThreads >= kTN && SA >= 2 && SB >= SA && kLater < 64, "scales: one per thread; vmcnt");
 };
 
 __device__ __forceinline__ v8i fragment(const v4i* tile, uint32_t row, uint32_t lane) {
@@ -485,9 +493,9 @@ __device__ void count_tiles(const int32_t* offs, int32_t G, int64_t M, uint32_t*
 // column by column, and XCD x takes a contiguous eighth: a column's B is read
 // into one L2 (two at a seam), for all its row tiles at once.  (Dealt out
 // tile by tile every B was read into several L2s: [8192, 8192] by 128, 512 and
-// 1024 rows took 39.1, 74.0 and 80.1 us instead of 25.5, 42.4 and 66.8.)  Row groups: XCD x takes a contiguous eighth of the covered
-// row tiles, all column tiles of a row tile in a row, then its eighth of the
-// tail.
+// 1024 rows took 39.1, 74.0 and 80.1 us instead of 25.5, 42.4 and 66.8.)  Row
+// groups: XCD x takes a contiguous eighth of the covered row tiles, all column
+// tiles of a row tile in a row, then its eighth of the tail.
 constexpr uint32_t kBand = 8;
 
 template <int TM>
@@ -519,18 +527,30 @@ __device__ bool place_tile(const I8Args& p, RowTile* r, uint32_t* tn) {
     return find_tile<TM>(p.offs, p.G, p.M, tm, r);
 }
 
-// The tile's scales and bias into LDS.
+// The tile's scales and bias: read by one thread each while the first steps are
+// on their way, put into LDS when the stages are free.
 template <typename P>
-__device__ __forceinline__ void load_scales(const I8Args& p, uint8_t* lds, const float* sB, const RowTile& r, int64_t n0,
-                                            uint32_t rows, uint32_t cols) {
-    const uint32_t t = threadIdx.x;
-    float* sc = reinterpret_cast<float*>(lds + P::kScales);
-    if (t < uint32_t(P::kTM)) sc[t] = p.sA[r.m0 + min(t, rows - 1u)];
-    if (t < uint32_t(P::kTN)) {
-        sc[P::kTM + t] = sB[min(t, cols - 1u)];
-        sc[P::kTM + P::kTN + t] = p.bias ? p.bias[n0 + min(t, cols - 1u)] : 0.f;
+struct Scales {
+    float a = 0.f, b = 0.f, bias = 0.f;
+    __device__ __forceinline__ void read(const I8Args& p, const float* sB, const RowTile& r, int64_t n0, uint32_t rows,
+                                         uint32_t cols) {
+        const uint32_t t = threadIdx.x;
+        if (t < uint32_t(P::kTM)) a = p.sA[r.m0 + min(t, rows - 1u)];
+        if (t < uint32_t(P::kTN)) {
+            b = sB[min(t, cols - 1u)];
+            if (p.bias) bias = p.bias[n0 + min(t, cols - 1u)];
+        }
     }
-}
+    __device__ __forceinline__ void write(uint8_t* lds) const {
+        const uint32_t t = threadIdx.x;
+        float* sc = reinterpret_cast<float*>(lds + P::kScales);
+        if (t < uint32_t(P::kTM)) sc[t] = a;
+        if (t < uint32_t(P::kTN)) {
+            sc[P::kTM + t] = b;
+            sc[P::kTM + P::kTN + t] = bias;
+        }
+    }
+};
 
 // A wave's staged rows (kCols columns at a pitch in bytes) to C: 16-byte
 // non-temporal stores where C allows them.
@@ -577,7 +597,7 @@ __device__ __forceinline__ void store_tile(const I8Args& p, const v4i (&acc)[MS]
     }
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
-        const uint32_t r0 = wm * 16u * MS + 16u * i;
+        const uint32_t r0 = 16u * (uint32_t(P::kWM) * i + wm);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const uint32_t row = 4u * (lane >> 4) + v;
@@ -598,9 +618,18 @@ __device__ __forceinline__ void store_tile(const I8Args& p, const v4i (&acc)[MS]
     }
 }
 
-template <typename O, int MS, int NS, int WM, int WN, int ST, bool kStreamB>
+// f(n) for a uniform n in [1, MS].
+template <int MS, typename F>
+__device__ __forceinline__ void each_count(uint32_t n, F&& f) {
+    if constexpr (MS > 1) {
+        if (n < uint32_t(MS)) return each_count<MS - 1>(n, f);
+    }
+    f(std::integral_constant<int, MS>{});
+}
+
+template <typename O, int MS, int NS, int WM, int WN, int SA, int SB, bool kGroups>
 __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
-    using P = Pipe<MS, NS, WM, WN, ST>;
+    using P = Pipe<MS, NS, WM, WN, SA, SB>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[P::kLds];
 
     const uint32_t t = threadIdx.x, lane = t & 63u;
@@ -629,14 +658,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
     for (int q = 0; q < P::kLB; ++q) vb[q] = min(8u * (uint32_t(P::kLB) * wave + q) + lr, cols - 1u) * ldb + lc;
     const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(lds));
     const uint32_t cut = K % 128u != 0 && lc >= K % 128u ? lc : 0u;          // the last step's pieces past K read piece 0
-    auto issue = [&](uint32_t step, uint32_t stage) {
-        const uint32_t k = step * 128u, st = lds0 + stage * P::kStage, back = step + 1u == n ? cut : 0u;
+    auto issue_a = [&](uint32_t step, uint32_t slot) {
+        const uint32_t k = step * 128u, back = step + 1u == n ? cut : 0u;
 #pragma unroll
-        for (int q = 0; q < P::kLA; ++q) pipe_load16(ra, st + 1024u * (uint32_t(P::kLA) * wave + q), va[q] - back, k);
+        for (int q = 0; q < P::kLA; ++q)
+            pipe_load16(ra, lds0 + slot * P::kStageA + 1024u * (uint32_t(P::kLA) * wave + q), va[q] - back, k);
+    };
+    auto issue_b = [&](uint32_t step, uint32_t slot) {
+        const uint32_t k = step * 128u, back = step + 1u == n ? cut : 0u;
 #pragma unroll
         for (int q = 0; q < P::kLB; ++q) {
-            const uint32_t at = st + P::kB + 1024u * (uint32_t(P::kLB) * wave + q);
-            if constexpr (kStreamB) pipe_load16_nt(rb, at, vb[q] - back, k);
+            const uint32_t at = lds0 + P::kB + slot * P::kStageB + 1024u * (uint32_t(P::kLB) * wave + q);
+            if constexpr (kGroups) pipe_load16_nt(rb, at, vb[q] - back, k);
             else pipe_load16(rb, at, vb[q] - back, k);
         }
     };
@@ -648,50 +681,64 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
         for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
 
 #pragma unroll
-    for (uint32_t s = 0; s + 1 < uint32_t(P::kStages); ++s)
-        if (s < n) issue(s, s);
-    load_scales<P>(p, lds, sB, r, n0, rows, cols);                          // while the first stage is on its way
-    uint32_t stage = 0;
-    for (uint32_t s = 0; s < n; ++s) {
-        // step s has arrived; the kStages - 2 after it may be under way (near the
-        // end, where fewer are, all are waited for)
-        if (P::kStages > 2 && s + P::kStages - 2 < n) pipe_sync<(P::kStages - 2) * P::kLoads>();
-        else pipe_sync<0>();
-        if (s + P::kStages - 1 < n) {
-            const uint32_t free = stage == 0 ? uint32_t(P::kStages - 1) : stage - 1u;
-            issue(s + P::kStages - 1, free);
-        }
-        uint8_t* st = lds + stage * P::kStage;
-        if (s + 1 == n && K % 128u != 0) {
-            const uint32_t c0 = K % 128u / 16u, left = 8u - c0;              // K is whole pieces
-            for (uint32_t c = t; c < left * uint32_t(P::kTM); c += uint32_t(P::kThreads)) {
-                const uint32_t row = c / left, piece = c0 + c % left;
-                reinterpret_cast<v4i*>(st)[row * 8u + (piece ^ (row & 7u))] = v4i{0, 0, 0, 0};
-            }
-            pipe_sync<0>();
-        }
-        const v4i* ta = reinterpret_cast<const v4i*>(st);
-        const v4i* tb = reinterpret_cast<const v4i*>(st + P::kB);
-        v8i a[MS];
-#pragma unroll
-        for (int i = 0; i < MS; ++i) a[i] = fragment(ta, wm * 16u * MS + 16u * i + (lane & 15u), lane);
-        v8i b = fragment(tb, wn * 16u * NS + (lane & 15u), lane);
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            v8i nb = b;
-            if (j + 1 < NS) nb = fragment(tb, wn * 16u * NS + 16u * (j + 1) + (lane & 15u), lane);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo4(a[i]), lo4(b), acc[i][j], 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi4(a[i]), hi4(b), acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            b = nb;
-        }
-        stage = stage + 1u == uint32_t(P::kStages) ? 0u : stage + 1u;
+    for (uint32_t s = 0; s + 1 < uint32_t(SB); ++s) {                       // as the steps before the first would
+        if (s + SA >= uint32_t(SB) && s + SA - SB < n) issue_a(s + SA - SB, s + SA - SB);
+        if (s < n) issue_b(s, s);
     }
+    Scales<P> scales;
+    scales.read(p, sB, r, n0, rows, cols);
+    // The contraction for the first I row fragments of every wave.
+    auto contract = [&](auto fragments) {
+        constexpr int I = decltype(fragments)::value;
+        uint32_t slot_a = 0, slot_b = 0;
+        for (uint32_t s = 0; s < n; ++s) {
+            // step s has arrived, and of what was issued later the most there can be
+            // is under way (near the end, where fewer are, all are waited for)
+            if (P::kLater > 0 && s + SB - 2 < n) pipe_sync<P::kLater>();
+            else pipe_sync<0>();
+            if (s + SA - 1 < n) issue_a(s + SA - 1, slot_a == 0 ? uint32_t(SA - 1) : slot_a - 1u);
+            if (s + SB - 1 < n) issue_b(s + SB - 1, slot_b == 0 ? uint32_t(SB - 1) : slot_b - 1u);
+            uint8_t* st = lds + slot_a * P::kStageA;
+            if (s + 1 == n && K % 128u != 0) {
+                const uint32_t c0 = K % 128u / 16u, left = 8u - c0;              // K is whole pieces
+                for (uint32_t c = t; c < left * uint32_t(P::kTM); c += uint32_t(P::kThreads)) {
+                    const uint32_t row = c / left, piece = c0 + c % left;
+                    reinterpret_cast<v4i*>(st)[row * 8u + (piece ^ (row & 7u))] = v4i{0, 0, 0, 0};
+                }
+                pipe_sync<0>();
+            }
+            const v4i* ta = reinterpret_cast<const v4i*>(st);
+            const v4i* tb = reinterpret_cast<const v4i*>(lds + P::kB + slot_b * P::kStageB);
+            v8i a[I];
+#pragma unroll
+            for (int i = 0; i < I; ++i) a[i] = fragment(ta, 16u * (uint32_t(WM) * i + wm) + (lane & 15u), lane);
+            v8i b = fragment(tb, wn * 16u * NS + (lane & 15u), lane);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                v8i nb = b;
+                if (j + 1 < NS) nb = fragment(tb, wn * 16u * NS + 16u * (j + 1) + (lane & 15u), lane);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo4(a[i]), lo4(b), acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi4(a[i]), hi4(b), acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                b = nb;
+            }
+            slot_a = slot_a + 1u == uint32_t(SA) ? 0u : slot_a + 1u;
+            slot_b = slot_b + 1u == uint32_t(SB) ? 0u : slot_b + 1u;
+        }
+    };
+    if constexpr (kGroups) {
+        const uint32_t need = (rows + 16u * WM - 1u) / (16u * WM);          // uniform
+        each_count<MS>(need, contract);
+    } else {
+        contract(std::integral_constant<int, MS>{});
+    }
+    __syncthreads();
+    scales.write(lds);
     __syncthreads();
 
     store_tile<O, MS, NS, P>(p, acc, lds, r, n0, rows, cols, wave, wm, wn, zero);
@@ -910,14 +957,14 @@ hipError_t launch_ring(I8Args& p, hipStream_t stream) {
 // ceiling of the covered tiles and one of the tail's.
 int64_t group_tiles(int64_t tiles_m) { return 8 * ((tiles_m + 7) / 8 + 1); }
 
-template <typename O, int MS, int NS, int WM, int WN, int ST, bool kStreamB>
+template <typename O, int MS, int NS, int WM, int WN, int SA, int SB, bool kGroups>
 hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
-    using P = Pipe<MS, NS, WM, WN, ST>;
+    using P = Pipe<MS, NS, WM, WN, SA, SB>;
     const int64_t tm = tile_bound(p.M, P::kTM, p.offs != nullptr, p.G);
     p.tiles_m = uint32_t(tm);
     p.tiles_n = uint32_t((p.N + P::kTN - 1) / P::kTN);
     const uint32_t blocks = p.offs ? uint32_t(group_tiles(tm)) * p.tiles_n : (uint32_t(tm) * p.tiles_n + 7u) / 8u * 8u;
-    hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, ST, kStreamB>), dim3(blocks), dim3(64 * WM * WN), 0,
+    hipLaunchKernelGGL((i8_pipe_kernel<O, MS, NS, WM, WN, SA, SB, kGroups>), dim3(blocks), dim3(64 * WM * WN), 0,
                        stream, p);
     return hipGetLastError();
 }
@@ -966,11 +1013,13 @@ struct Form {
 //
 // Row groups, by the mean rows of a group (64 experts of [2048, 5120], group
 // sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows):
-//   rows   4: 108.0  117.6         rows  48: 141.8  147.3  156.3
-//   rows  16: 107.6  113.9         rows 128: 234.1  173.5  201.1
-//   rows  24: 134.7  113.1  159.4  rows 192:        229.1  214.0
-//   rows  32: 135.3  115.0  153.9  rows 384:        394.6  320.1
-// (the 671 MB of weights alone take 108 us at 6.2 TB/s).
+//   rows   8: 106.3  111.9  126.6  rows  96:        154.7  169.6
+//   rows  16: 108.4  112.8  125.5  rows 128:        164.1  175.3
+//   rows  24: 133.7  113.4  124.4  rows 192:        217.3  204.4
+//   rows  32: 135.1  116.8  131.9  rows 256:        262.9  236.8
+//   rows  64:        152.9  137.6  rows 512:        482.1  411.4
+// (64 rows to each expert alike: 120.8 and 136.0; the 671 MB of weights alone
+// take 108 us at 6.2 TB/s).
 //
 // Dense: the piped tile with the least ceil(tiles / 256 CUs) (steps t + 1.2
 // us), t the time of one 128-code step: 256 x 256 1.25 us, 128 x 256 0.80,
@@ -1036,15 +1085,15 @@ hipError_t launch(I8Args& p, hipStream_t stream) {
         // the hint, 126 without, at 24 rows a group); dense tiles meet in the L2
         // (428 us without, 470 with it, for 8192 cubed)
         if (p.offs) {
-            if (f.ms == 1) return launch_pipe<O, 2, 4, 2, 4, 3, true>(p, stream);
-            if (f.ms == 2) return launch_pipe<O, 4, 4, 2, 4, 3, true>(p, stream);
-            return launch_pipe<O, 4, 8, 4, 2, 2, true>(p, stream);
+            if (f.ms == 1) return launch_pipe<O, 2, 4, 2, 4, 3, 3, true>(p, stream);
+            if (f.ms == 2) return launch_pipe<O, 4, 4, 2, 4, 2, 4, true>(p, stream);
+            return launch_pipe<O, 4, 8, 4, 2, 2, 3, true>(p, stream);
         }
-        if (f.ms == 4) return launch_pipe<O, 4, 8, 4, 2, 2, false>(p, stream);
-        if (f.ms == 1) return launch_pipe<O, 1, 2, 4, 2, 4, false>(p, stream);
-        if (f.ns == 4) return launch_pipe<O, 4, 4, 2, 4, 3, false>(p, stream);
-        if (f.ns == 2) return launch_pipe<O, 2, 4, 4, 2, 4, false>(p, stream);
-        return launch_pipe<O, 2, 2, 4, 2, 6, false>(p, stream);
+        if (f.ms == 4) return launch_pipe<O, 4, 8, 4, 2, 2, 2, false>(p, stream);
+        if (f.ms == 1) return launch_pipe<O, 1, 2, 4, 2, 4, 4, false>(p, stream);
+        if (f.ns == 4) return launch_pipe<O, 4, 4, 2, 4, 3, 3, false>(p, stream);
+        if (f.ns == 2) return launch_pipe<O, 2, 4, 4, 2, 4, 4, false>(p, stream);
+        return launch_pipe<O, 2, 2, 4, 2, 6, 6, false>(p, stream);
     }
     if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
     switch (f.ms * 8 + f.ns) {
