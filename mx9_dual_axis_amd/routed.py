@@ -197,7 +197,8 @@ def mx_route(logits: torch.Tensor, k: int | None = None, valid: torch.Tensor | N
     valid (bool or uint8 [T]) leaves tokens out, a logit of -inf an expert.
     The result's weight are the picks' probabilities, over their sum when
     `normalize`; counts, offs, slot and src describe the padded buffer that
-    the grouped casts and products take; loss is the balance loss."""
+    the grouped casts and products take; loss is the balance loss.  With out (an
+    MXRouting) k and align are those it was made for."""
     ld = _matrix(logits, "logits", _ESZ)
     T, E = logits.shape
     dev = logits.device
