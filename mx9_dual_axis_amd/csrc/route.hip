@@ -329,7 +329,7 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouteArgs p) {
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
     const L* logits = static_cast<const L*>(p.logits);
     // Scores are read a round ahead where the registers allow it at four waves a
-    // SIMD (the three kernels, without and with it: 131072 tokens of 256 fp32
+    // SIMD and a block has several rounds (the three kernels, without and with it: 131072 tokens of 256 fp32
     // scores 72.6 and 71.5 us, of 64 bf16 scores 37.1 and 35.8, 65536 of 160
     // 39.3 and 36.7).
     constexpr bool kAhead = V <= 16 && kThr == 256;
@@ -713,35 +713,59 @@ struct RouteGradArgs {
 
 constexpr int kGradThr = 256;
 
+// The gradient reads logits and writes dlogits once: HBM bounds it, at the
+// latency of a row's loads.  A row's memory is therefore read a round ahead
+// (up to 256 experts, where the registers allow four waves a SIMD), and the
+// loss's part of each expert stays in LDS, not in registers.  131072 tokens of
+// 256 fp32 scores take 51 us (their bytes alone, as a copy's, 54; 58 without
+// either measure), of 256 bf16 scores 42 (27; 59), 65536 of 384 bf16 scores 40
+// (20; 90).
 template <typename L, int V>
 __global__ __launch_bounds__(kGradThr) void route_grad_kernel(RouteGradArgs p) {
     using S = Scores<L, V>;
     constexpr int kC = S::kC;
     __shared__ __attribute__((aligned(16))) float up[kGradThr / 16][16 * V];   // each row's own wave alone uses it
+    __shared__ __attribute__((aligned(16))) float share[16 * V];           // the loss's part of each expert
     const uint32_t t = threadIdx.x, l16 = t & 15u, grp = t >> 4;
+    const bool whole = p.E == 16 * V, picks = p.dweight != nullptr && l16 < uint32_t(p.k);
+    // what a row takes from memory, read a round ahead
+    L ahead[V];
+    uint8_t take = 1;
+    int32_t e_ahead = -1;
+    float c_ahead = 0.f, w_ahead = 0.f;
+    auto fetch = [&](int64_t at, uint32_t l16) {
+        if (p.valid) take = p.valid[at];
+        if (whole) fetch_row<L, V, true>(static_cast<const L*>(p.logits) + at * p.ld, l16, p.E, ahead);
+        else fetch_row<L, V, false>(static_cast<const L*>(p.logits) + at * p.ld, l16, p.E, ahead);
+        if (picks) {
+            e_ahead = p.idx[at * p.k + l16];
+            c_ahead = p.dweight[at * p.k + l16];
+            w_ahead = p.weight[at * p.k + l16];
+        }
+    };
+    int64_t row = int64_t(blockIdx.x) * (kGradThr / 16) + grp;
+    const int64_t step = int64_t(gridDim.x) * (kGradThr / 16);
+    constexpr bool kAhead = V <= 16;
+    if (kAhead) fetch(row < p.T ? row : p.T - 1, l16);
     const float n = float(max(p.live[0], 1));
     const float unit = p.dloss ? p.dloss[0] * float(p.E) / (float(p.k) * n * n) : 0.f;
-    float a[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int32_t e = S::expert(l16, v);
-        a[v] = e < p.E ? unit * float(p.counts[e]) : 0.f;
-    }
-    for (int64_t row = int64_t(blockIdx.x) * (kGradThr / 16) + grp; row < p.T; row += int64_t(gridDim.x) * (kGradThr / 16)) {
+    for (uint32_t e = t; e < 16u * V; e += kGradThr) share[e] = int32_t(e) < p.E ? unit * float(p.counts[e]) : 0.f;
+    __syncthreads();
+    for (; row < p.T; row += step) {
+        uint32_t l16 = t & 15u;                                             // formed anew, as in routing
+        asm volatile("" : "+v"(l16));
+        if (!kAhead) fetch(row, l16);
         float z[V], q[V];
-        const bool in = (p.valid ? p.valid[row] : uint8_t(1)) != 0;
-        load_row<L, V>(static_cast<const L*>(p.logits) + row * p.ld, l16, p.E, z);
-        int32_t e = -1;
-        float c = 0.f, w = 0.f;
-        if (p.dweight != nullptr && l16 < uint32_t(p.k)) {
-            e = p.idx[row * p.k + l16];
-            c = p.dweight[row * p.k + l16];
-            w = p.weight[row * p.k + l16];
-            if (uint32_t(e) >= uint32_t(p.E)) {
-                e = -1;
-                c = w = 0.f;
-            }
+        const bool in = take != 0;
+        if (whole) widen_row<L, V, true>(ahead, l16, p.E, z);
+        else widen_row<L, V, false>(ahead, l16, p.E, z);
+        int32_t e = e_ahead;
+        float c = c_ahead, w = w_ahead;
+        if (uint32_t(e) >= uint32_t(p.E)) {
+            e = -1;
+            c = w = 0.f;
         }
+        if (kAhead && row + step < p.T) fetch(row + step, l16);
         // the picks' direct part, scattered over the row through LDS
         float d[V];
         if (p.dweight != nullptr) {
@@ -770,7 +794,8 @@ __global__ __launch_bounds__(kGradThr) void route_grad_kernel(RouteGradArgs p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             q[v] *= r.inv;
-            s += q[v] * (p.normalize ? a[v] : a[v] + d[v]);
+            const float a = share[S::expert(l16, v)];
+            s += q[v] * (p.normalize ? a : a + d[v]);
         }
         s = row_sum(s);
         L* out = static_cast<L*>(p.dlogits) + row * p.ld_d;
@@ -781,7 +806,8 @@ __global__ __launch_bounds__(kGradThr) void route_grad_kernel(RouteGradArgs p) {
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
                 const int v = b * kC + i;
-                const float g = p.normalize ? q[v] * (a[v] - s) + d[v] : q[v] * (a[v] + d[v] - s);
+                const float a = share[e0 + i];
+                const float g = p.normalize ? q[v] * (a - s) + d[v] : q[v] * (a + d[v] - s);
                 o[i] = narrow<L>(r.live ? g : 0.f);
             }
             if (e0 + kC <= p.E) {
@@ -802,9 +828,15 @@ hipError_t run_first(const RouteArgs& p, hipStream_t stream) {
         hipLaunchKernelGGL((route_kernel<L, V, kKeep, 64>), grid, dim3(64), 0, stream, p);
         return hipGetLastError();
     }
-    if constexpr (V <= 8) {
-        if (p.passes == 1) {
-            hipLaunchKernelGGL((route_kernel<L, V, kKeep, 1024>), grid, dim3(1024), 0, stream, p);
+    // Few blocks of many threads hide more of their loads: up to 512 blocks of up
+    // to 128 experts, up to a block a CU beyond (256, 512 and 1024 threads, the
+    // three kernels: 16384 x 256 fp32 29.6, 24.8 and 24.4 us, 4096 x 256 26.2, 21.3
+    // and 20.4, 8192 x 512 40.5, 32.4 and 40.7; but 32768 x 256 34.5, 37.4 and 36.7,
+    // and 131072 x 256 71.5, 97.3 and 96.5).
+    constexpr int kMany = V <= 16 ? 1024 : 512;
+    if constexpr (V <= 32) {
+        if (V <= 8 ? p.passes == 1 : p.blocks <= 256) {
+            hipLaunchKernelGGL((route_kernel<L, V, kKeep, kMany>), grid, dim3(kMany), 0, stream, p);
             return hipGetLastError();
         }
     }
@@ -826,7 +858,9 @@ hipError_t route_first(const RouteArgs& p, hipStream_t stream) {
 template <typename L>
 hipError_t route_grad(const RouteGradArgs& p, hipStream_t stream) {
     const int64_t blocks = (p.T + 15) / 16;
-    const dim3 grid(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)), block(kGradThr);
+    // 1024, 2048 and 4096 blocks: 128.9, 126.4 and 127.7 us for routing and
+    // gradient of 131072 tokens of 256 fp32 scores
+    const dim3 grid(static_cast<uint32_t>(blocks < 2048 ? blocks : 2048)), block(kGradThr);
     if (p.E <= 16) hipLaunchKernelGGL((route_grad_kernel<L, 1>), grid, block, 0, stream, p);
     else if (p.E <= 32) hipLaunchKernelGGL((route_grad_kernel<L, 2>), grid, block, 0, stream, p);
     else if (p.E <= 64) hipLaunchKernelGGL((route_grad_kernel<L, 4>), grid, block, 0, stream, p);
