@@ -18,6 +18,19 @@
 // numbered group by group (a group's tiles start at its first row), the tail
 // as a last group; every wave finds its tile's group by a prefix sum over
 // 64 group ends at a time.
+//
+// Forms, from few rows to many (choose() has the rules and both sides of each):
+//   ring   up to 16 rows: bound by the weights' one way from HBM; each wave
+//          streams its share through LDS for itself.  One token through [14336,
+//          4096]: 12.1 us, its quantization within, 58.7 MB at 4.9 TB/s.
+//   pipe   operands in whole 16-byte pieces: tiles of 64 x 64 to 256 x 256,
+//          loads straight to LDS.  8192 cubed: 430 to 490 us (2.2 to 2.6 PFLOP/s;
+//          the clock falls as the matrix cores fill), 64 experts of [2048, 5120]
+//          with 2 rows each 87 us (the weights' 580 MB), with 256 245 us.
+//   split  rows that start at any byte, few tiles: the waves of a workgroup
+//          split the contraction.  77 x 1000 x 1111: 5.2 us.
+//   tiles  rows that start at any byte, many tiles: staged through registers.
+//          512 x 8191 x 4095: 70.7 us.
 #include "mxq_kernels.h"
 
 #include <type_traits>

@@ -118,7 +118,8 @@ struct DispatchArgs {
 constexpr int64_t kChunk = 4096;
 
 // One wave per token and 4 KiB chunk of its row, then one wave per 16 rows of
-// the map and chunk for the rows without a token.
+// the map and chunk for the rows without a token.  [4096, 5120] bf16 to 24576
+// rows, 4 picks a token: 49 us, 293.6 MB at 6.0 TB/s.
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs p) {
     const uint32_t lane = threadIdx.x & 63u;
     const int64_t w = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -186,7 +187,8 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
 
 // One block per token: the largest magnitude, then codes.  kHold pieces of
 // the row stay in each thread's registers between the two; a longer row's
-// rest is read again, from the cache.
+// rest is read again, from the cache.  [8192, 8192] bf16: 39 us, 201 MB at 5.2
+// TB/s; [4096, 5120] bf16 to 24576 rows 31 us, 168 MB at 5.4 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
     constexpr int kPer = Elem<T>::kPer, kHold = 4;
@@ -290,7 +292,10 @@ struct CombineArgs {
     int64_t chunks;              // 64-piece chunks per row
 };
 
-// One wave per token and 64 pieces of its row.
+// One wave per token and 64 pieces of its row.  4096 tokens of 4 rows of 5120
+// in bf16: 38 us when called over and over, 210 MB at 5.5 TB/s (48 to 55 us
+// among other kernels).  Reading four rows before the first is added gained
+// nothing there (38.2 us) and cost half again with one row (19.8 us for 13.8).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs p) {
     constexpr int kPer = Elem<T>::kPer;
@@ -343,7 +348,8 @@ struct CombineGradArgs {
     float* dweight;
 };
 
-// One block per token: dy stays in registers over the token's rows.
+// One block per token: dy stays in registers over the token's rows.  4096 tokens
+// of 4 rows of 5120 in bf16, 24576 rows written: 84 us, 462 MB at 5.5 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs p) {
     constexpr int kPer = Elem<T>::kPer, kHold = 4;
