@@ -101,7 +101,7 @@ int mx_route_grad(const void *logits, int32_t dtype, int64_t T, int32_t E, int64
  *
  * mx_dispatch_i8 -- the same with each row quantized: q int8 [M, K] (pitch
  * ld_q >= K), s f32 [M].  With a = max(max |x|, 127 2^-126):
- * q = round-half-even(x (127 / a)), s = a / 127 (each operation rounded to
+ * q = round-half-even(x (127 (1 / a))), s = a / 127 (each operation rounded to
  * fp32).  A row with Inf or NaN: q = 0, s = NaN.
  *
  * i8_quantize_rows -- mx_dispatch_i8 without a map: q [T, K], s [T] (rows are

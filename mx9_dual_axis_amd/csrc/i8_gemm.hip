@@ -850,7 +850,7 @@ __device__ __forceinline__ void quantize_to_lds(const I8Args& p, uint8_t* raw, u
     for (int i = 0; i < kHold; ++i) {
         if (uint32_t(i * kThr) >= pieces) break;
         const uint32_t m = maxes[row[i]];
-        const float inv = 127.f / fmaxf(__uint_as_float(m), 127.f * 0x1p-126f);
+        const float inv = 127.f * (1.f / fmaxf(__uint_as_float(m), 127.f * 0x1p-126f));
         uint32_t* at = reinterpret_cast<uint32_t*>(codes + row[i] * pitch + piece[i] * kPer);
 #pragma unroll
         for (int q = 0; q < kPer / 4; ++q) {

@@ -3,7 +3,7 @@
 // combine and its gradient.
 //
 //   dispatch      out[slot[t][j]] = x[t]                     rows without a token: 0
-//   quantize      a = max(max |x|, 127 2^-126), q = rne(x (127 / a)), s = a / 127
+//   quantize      a = max(max |x|, 127 2^-126), q = rne(x (127 (1 / a))), s = a / 127
 //                 (a row with Inf or NaN: q = 0, s = NaN, so that what is
 //                 computed from it is NaN)
 //   combine       y[t] = sum_j w[t][j] rows[slot[t][j]]      fp32, j ascending, rounded once
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
     m = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
     const bool bad = m >= 0x7F800000u;
     const float a = fmaxf(__uint_as_float(m), kFloor);
-    const float inv = bad ? 0.f : 127.f / a;
+    const float inv = bad ? 0.f : 127.f * (1.f / a);                        // as torch forms 127 / a: the same codes
     const float s = bad ? __uint_as_float(0x7FC00000u) : a / 127.f;
 
     auto put = [&](int64_t c, u32x4 v) {

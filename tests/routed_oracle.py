@@ -105,7 +105,7 @@ def quantize(x):
             s[t] = np.nan
             continue
         a = np.float32(max(np.abs(x[t]).max() if K else np.float32(0), floor))
-        q[t] = np.rint(x[t] * np.float32(np.float32(127) / a)).astype(np.int8)
+        q[t] = np.rint(x[t] * np.float32(np.float32(127) * np.float32(np.float32(1) / a))).astype(np.int8)
         s[t] = np.float32(a / np.float32(127))
     return q, s
 
