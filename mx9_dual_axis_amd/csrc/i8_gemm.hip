@@ -29,8 +29,8 @@
 //          with 2 rows each 87 us (the weights' 580 MB), with 256 245 us.
 //   split  rows that start at any byte, few tiles: the waves of a workgroup
 //          split the contraction.  77 x 1000 x 1111: 5.2 us.
-//   tiles  rows that start at any byte, many tiles: staged through registers.
-//          512 x 8191 x 4095: 70.7 us.
+//   staged rows that start at any byte, many tiles: as pipe, through registers.
+//          512 x 8191 x 4095: 36 us.
 #include "mxq_kernels.h"
 
 #include <type_traits>
@@ -163,108 +163,6 @@ template <> struct Out<float> {
 template <> struct Out<__bf16> {
     static __device__ __forceinline__ __bf16 get(float x) { return __bf16(x); }   // nearest-even
 };
-
-// ---- any shape, pitch and alignment: 128 x 128 tiles, 128 codes a step ----
-//
-// 4 waves, each a 64 x 64 quarter (4 x 4 instructions, twice per step).  The
-// next step's 16-byte pieces wait in registers while this one's are
-// multiplied from LDS, whose rows of 8 pieces are stored under an XOR of the
-// piece with the row (mod 8), so that neither side conflicts.
-constexpr int kTile = 128;
-
-template <typename O>
-__global__ __launch_bounds__(256, 2) void i8_gemm_kernel(I8Args p) {
-    __shared__ v4i lds[2][2][kTile * 8];
-    const uint32_t t = threadIdx.x, lane = t & 63u, wave = t >> 6;
-    const uint32_t wm = wave >> 1, wn = wave & 1u;
-    const uint32_t tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
-    RowTile r;
-    if (!find_tile<kTile>(p.offs, p.G, p.M, tm, &r)) return;       // uniform
-    const int64_t n0 = int64_t(tn) * kTile;
-    const bool zero = p.offs != nullptr && r.g >= p.G;
-    const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs);
-    const float* sB = p.sB + (zero ? 0 : int64_t(r.g) * p.sb_gs);
-
-    v4i acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-
-    if (!zero) {
-        // this thread's pieces: rows r0 + 32 i, piece ch; rows past the end repeat the last
-        const uint32_t r0 = t >> 3, ch = t & 7u;
-        const int8_t *ga[4], *gb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t ar = r.m0 + r0 + 32 * i, br = n0 + r0 + 32 * i;
-            ga[i] = p.A + (ar < r.m1 ? ar : r.m1 - 1) * p.lda;
-            gb[i] = B + (br < p.N ? br : p.N - 1) * p.ldb;
-        }
-        const uint32_t slot = r0 * 8u + (ch ^ (r0 & 7u));
-        v4i va[4], vb[4];
-        auto load = [&](int64_t k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                va[i] = k + 128 <= p.K ? load16(ga[i] + k + 16 * ch) : load_codes(ga[i], k + 16 * ch, p.K, p.K);
-                vb[i] = k + 128 <= p.K ? load16(gb[i] + k + 16 * ch) : load_codes(gb[i], k + 16 * ch, p.K, p.K);
-            }
-        };
-        auto store = [&](int b) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lds[b][0][slot + 256 * i] = va[i];
-                lds[b][1][slot + 256 * i] = vb[i];
-            }
-        };
-        load(0);
-        store(0);
-        __syncthreads();
-        int buf = 0;
-        for (int64_t k = 0; k < p.K; k += 128) {
-            const bool more = k + 128 < p.K;
-            if (more) load(k + 128);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                v4i af[4], bf[4];
-                const uint32_t piece = 4u * h + (lane >> 4);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t ar = wm * 64 + 16 * s + (lane & 15u), br = wn * 64 + 16 * s + (lane & 15u);
-                    af[s] = lds[buf][0][ar * 8u + (piece ^ (ar & 7u))];
-                    bf[s] = lds[buf][1][br * 8u + (piece ^ (br & 7u))];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
-            }
-            if (more) store(buf ^ 1);
-            __syncthreads();
-            buf ^= 1;
-        }
-    }
-
-    O* C = static_cast<O*>(p.C);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t col = n0 + wn * 64 + 16 * j + (lane & 15u);
-        if (col >= p.N) continue;
-        const float sb = sB[col], bi = p.bias ? p.bias[col] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t row = r.m0 + wm * 64 + 16 * i + 4 * (lane >> 4) + v;
-                if (row >= r.m1) continue;
-                float x = float(acc[i][j][v]) * p.sA[row];
-                x = p.bias ? __builtin_fmaf(x, sb, bi) : x * sb;
-                C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : x);
-            }
-        }
-    }
-}
 
 // ---- few tiles, any alignment: every wave for itself ----
 //
@@ -565,8 +463,9 @@ struct Scales {
     }
 };
 
-// A wave's staged rows (kCols columns at a pitch in bytes) to C: 16-byte
-// non-temporal stores where C allows them.
+// A wave's staged rows (kCols columns at a pitch in bytes) to C in 16-byte
+// pieces: non-temporal where C has them whole, else through the L2, where
+// neighbours meet (4000 x 5001 x 333: 35 us so, 61 by element).
 template <typename O, int kCols, int kRows>
 __device__ __forceinline__ void store_rows(const I8Args& p, const uint8_t* ep, int pitch, int64_t row0, int64_t col0,
                                            uint32_t rows, uint32_t cols) {
@@ -580,10 +479,11 @@ __device__ __forceinline__ void store_rows(const I8Args& p, const uint8_t* ep, i
         const uint8_t* from = ep + row * pitch + col * sizeof(O);
         if (row >= rows || col >= cols) continue;
         O* to = C + (row0 + row) * p.ldc + col0 + col;
-        if (whole && col + kPer <= cols) {
+        if (col + kPer <= cols) {
             const uint4 val = *reinterpret_cast<const uint4*>(from);
             const u32x4 vv = {val.x, val.y, val.z, val.w};
-            __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(to));
+            if (whole) __builtin_nontemporal_store(vv, reinterpret_cast<u32x4*>(to));
+            else __builtin_memcpy(to, &vv, 16);
         } else {
 #pragma unroll 1
             for (uint32_t e = 0; e < kPer && col + e < cols; ++e) to[e] = reinterpret_cast<const O*>(from)[e];
@@ -628,6 +528,30 @@ __device__ __forceinline__ void store_tile(const I8Args& p, const v4i (&acc)[MS]
         store_rows<O, 16 * NS, 16>(p, ep, kPitch, r.m0 + r0, n0 + c0, rows - min(rows, r0), cols - min(cols, c0));
         __builtin_amdgcn_s_waitcnt(0xC07F);                                 // reads done before the next rows' writes
         __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// One step of a wave: its first I row fragments by all its columns.
+template <int I, int MS, int NS, int WM>
+__device__ __forceinline__ void multiply(const v4i* ta, const v4i* tb, v4i (&acc)[MS][NS], uint32_t wm, uint32_t wn,
+                                         uint32_t lane) {
+    v8i a[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) a[i] = fragment(ta, 16u * (uint32_t(WM) * i + wm) + (lane & 15u), lane);
+    v8i b = fragment(tb, wn * 16u * NS + (lane & 15u), lane);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        v8i nb = b;
+        if (j + 1 < NS) nb = fragment(tb, wn * 16u * NS + 16u * (j + 1) + (lane & 15u), lane);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo4(a[i]), lo4(b), acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi4(a[i]), hi4(b), acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        b = nb;
     }
 }
 
@@ -722,24 +646,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
             }
             const v4i* ta = reinterpret_cast<const v4i*>(st);
             const v4i* tb = reinterpret_cast<const v4i*>(lds + P::kB + slot_b * P::kStageB);
-            v8i a[I];
-#pragma unroll
-            for (int i = 0; i < I; ++i) a[i] = fragment(ta, 16u * (uint32_t(WM) * i + wm) + (lane & 15u), lane);
-            v8i b = fragment(tb, wn * 16u * NS + (lane & 15u), lane);
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                v8i nb = b;
-                if (j + 1 < NS) nb = fragment(tb, wn * 16u * NS + 16u * (j + 1) + (lane & 15u), lane);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < I; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo4(a[i]), lo4(b), acc[i][j], 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < I; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi4(a[i]), hi4(b), acc[i][j], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-                b = nb;
-            }
+            multiply<I, MS, NS, WM>(ta, tb, acc, wm, wn, lane);
             slot_a = slot_a + 1u == uint32_t(SA) ? 0u : slot_a + 1u;
             slot_b = slot_b + 1u == uint32_t(SB) ? 0u : slot_b + 1u;
         }
@@ -750,6 +657,93 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
     } else {
         contract(std::integral_constant<int, MS>{});
     }
+    __syncthreads();
+    scales.write(lds);
+    __syncthreads();
+
+    store_tile<O, MS, NS, P>(p, acc, lds, r, n0, rows, cols, wave, wm, wn, zero);
+}
+
+// ---- many tiles, rows that start at any byte: pipelined through registers ----
+//
+// The tiles, LDS layout and steps of the form above, but a thread's pieces come
+// by ordinary loads (which take any address), wait in registers through the
+// step before theirs, and are written to the slot that the step before that one
+// has left.  Near a row's end the row's last piece is shifted, zeros behind it.
+template <typename O, int MS, int NS, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void i8_staged_kernel(I8Args p) {
+    using P = Pipe<MS, NS, WM, WN, 2, 2>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[P::kLds];
+
+    const uint32_t t = threadIdx.x, lane = t & 63u;
+    const uint32_t wave = uint32_t(uniform(int32_t(t >> 6)));
+    const uint32_t wm = wave / WN, wn = wave % WN;
+
+    RowTile r;
+    uint32_t tn;
+    if (!place_tile<P::kTM>(p, &r, &tn)) return;                            // uniform
+    const bool zero = p.offs != nullptr && r.g >= p.G;
+    const int64_t n0 = int64_t(tn) * P::kTN;
+    const uint32_t rows = uint32_t(min(int64_t(P::kTM), r.m1 - r.m0)), cols = uint32_t(min(int64_t(P::kTN), p.N - n0));
+    const int8_t* A = p.A + r.m0 * p.lda;
+    const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs) + n0 * p.ldb;
+    const float* sB = p.sB + (zero ? 0 : int64_t(r.g) * p.sb_gs) + n0;
+    const uint32_t K = uint32_t(p.K), n = zero ? 0u : (K + 127u) / 128u;
+
+    const uint32_t lda = uint32_t(p.lda), ldb = uint32_t(p.ldb);
+    const uint32_t lr = lane >> 3, lc = 16u * ((lane & 7u) ^ lr);
+    uint32_t va[P::kLA], vb[P::kLB];                                        // of the tile: below 2^31
+#pragma unroll
+    for (int q = 0; q < P::kLA; ++q) va[q] = min(8u * (uint32_t(P::kLA) * wave + q) + lr, rows - 1u) * lda + lc;
+#pragma unroll
+    for (int q = 0; q < P::kLB; ++q) vb[q] = min(8u * (uint32_t(P::kLB) * wave + q) + lr, cols - 1u) * ldb + lc;
+    v4i ha[P::kLA], hb[P::kLB];
+    auto load = [&](uint32_t step) {
+        const uint32_t k = step * 128u;
+        if (k + 128u <= K) {                                                // uniform
+            const int8_t *a = A + k, *b = B + k;
+#pragma unroll
+            for (int q = 0; q < P::kLA; ++q) ha[q] = load16(a + va[q]);
+#pragma unroll
+            for (int q = 0; q < P::kLB; ++q) hb[q] = load16(b + vb[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < P::kLA; ++q) ha[q] = load_codes(A + (va[q] - lc), k + lc, K, K);
+#pragma unroll
+            for (int q = 0; q < P::kLB; ++q) hb[q] = load_codes(B + (vb[q] - lc), k + lc, K, K);
+        }
+    };
+    auto put = [&](uint32_t slot) {
+        v4i* a = reinterpret_cast<v4i*>(lds + slot * P::kStageA) + lane;
+        v4i* b = reinterpret_cast<v4i*>(lds + P::kB + slot * P::kStageB) + lane;
+#pragma unroll
+        for (int q = 0; q < P::kLA; ++q) a[64u * (uint32_t(P::kLA) * wave + q)] = ha[q];
+#pragma unroll
+        for (int q = 0; q < P::kLB; ++q) b[64u * (uint32_t(P::kLB) * wave + q)] = hb[q];
+    };
+
+    v4i acc[MS][NS];
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+    Scales<P> scales;
+    if (n > 0) load(0);
+    scales.read(p, sB, r, n0, rows, cols);
+    if (n > 0) put(0);
+    if (n > 1) load(1);
+    auto contract = [&](auto fragments) {
+        constexpr int I = decltype(fragments)::value;
+        for (uint32_t s = 0; s < n; ++s) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // step s is in LDS; loads stay under way
+            if (s + 1 < n) put((s + 1) & 1u);
+            if (s + 2 < n) load(s + 2);
+            multiply<I, MS, NS, WM>(reinterpret_cast<const v4i*>(lds + (s & 1u) * P::kStageA),
+                                    reinterpret_cast<const v4i*>(lds + P::kB + (s & 1u) * P::kStageB), acc, wm, wn, lane);
+        }
+    };
+    each_count<MS>((rows + 16u * WM - 1u) / (16u * WM), contract);          // uniform
     __syncthreads();
     scales.write(lds);
     __syncthreads();
@@ -982,21 +976,23 @@ hipError_t launch_pipe(I8Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <typename O, int MS, int NS, int WM, int WN>
+hipError_t launch_staged(I8Args& p, hipStream_t stream) {
+    using P = Pipe<MS, NS, WM, WN, 2, 2>;
+    const int64_t tm = tile_bound(p.M, P::kTM, p.offs != nullptr, p.G);
+    p.tiles_m = uint32_t(tm);
+    p.tiles_n = uint32_t((p.N + P::kTN - 1) / P::kTN);
+    const uint32_t blocks = p.offs ? uint32_t(group_tiles(tm)) * p.tiles_n : (uint32_t(tm) * p.tiles_n + 7u) / 8u * 8u;
+    hipLaunchKernelGGL((i8_staged_kernel<O, MS, NS, WM, WN>), dim3(blocks), dim3(64 * WM * WN), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <typename O, int MS, int NS, int kW>
 hipError_t launch_split(I8Args& p, hipStream_t stream) {
     p.tiles_m = uint32_t(tile_bound(p.M, 16 * MS, p.offs != nullptr, p.G));
     p.tiles_n = uint32_t((p.N + 16 * NS - 1) / (16 * NS));
     const dim3 grid(p.tiles_m * p.tiles_n), block(64 * kW);
     hipLaunchKernelGGL((i8_split_kernel<O, MS, NS, kW>), grid, block, 0, stream, p);
-    return hipGetLastError();
-}
-
-template <typename O>
-hipError_t launch_tiles(I8Args& p, hipStream_t stream) {
-    p.tiles_m = uint32_t(tile_bound(p.M, kTile, p.offs != nullptr, p.G));
-    p.tiles_n = uint32_t((p.N + kTile - 1) / kTile);
-    const dim3 grid(p.tiles_m * p.tiles_n), block(256);
-    hipLaunchKernelGGL(i8_gemm_kernel<O>, grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1015,17 +1011,41 @@ hipError_t ring(I8Args& p, hipStream_t stream) {
 }
 
 // Which kernel.
-enum class Kind { kSplit, kTiles, kRing, kPipe };
+enum class Kind { kSplit, kStaged, kRing, kPipe };
 struct Form {
     Kind kind;
-    int ms, ns;                  // kSplit: 16-row, 16-column sub-tiles of a workgroup; kPipe: 64-row, 64-column units
+    int ms, ns;                  // kSplit: 16-row, 16-column sub-tiles of a workgroup; kStaged, kPipe: 64-row, 64-column units
     uint64_t threads;            // of the grid
 };
 
-// pipe: the operands are whole aligned 16-byte pieces.
-//
-// Row groups, by the mean rows of a group (64 experts of [2048, 5120], group
-// sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows):
+// What the operands allow: whole aligned 16-byte pieces, rows at any byte, rows
+// so far apart that a tile's offsets leave 32 bits.
+enum class Rows { kPieces, kBytes, kFar };
+bool far(int64_t lda, int64_t ldb) { return lda >= (1 << 23) || ldb >= (1 << 23); }
+
+// The tile with the least ceil(tiles / 256 CUs) (steps t + 1.2 us), t the time
+// of one 128-code step with a tile on each CU.
+struct Tile {
+    int um, un;                  // 64-row, 64-column units
+    double step;                 // us
+};
+template <int kN>
+const Tile& best_tile(const Tile (&tiles)[kN], int64_t M, int64_t N, int64_t K, int64_t groups) {
+    const Tile* best = nullptr;
+    double least = 0;
+    for (const Tile& t : tiles) {
+        const int64_t n = groups * ((M + 64 * t.um - 1) / (64 * t.um)) * ((N + 64 * t.un - 1) / (64 * t.un));
+        const double cost = double((n + 255) / 256) * (double((K + 127) / 128) * t.step + 1.2);
+        if (!best || cost < least) {
+            best = &t;
+            least = cost;
+        }
+    }
+    return *best;
+}
+
+// Row groups in whole pieces, by the mean rows of a group (64 experts of [2048,
+// 5120], group sizes spread by e^0.6; us for tiles of 64, 128 and 256 rows):
 //   rows   8: 106.3  111.9  126.6  rows  96:        154.7  169.6
 //   rows  16: 108.4  112.8  125.5  rows 128:        164.1  175.3
 //   rows  24: 133.7  113.4  124.4  rows 192:        217.3  204.4
@@ -1034,64 +1054,59 @@ struct Form {
 // (64 rows to each expert alike: 120.8 and 136.0; the 671 MB of weights alone
 // take 108 us at 6.2 TB/s).
 //
-// Dense: the piped tile with the least ceil(tiles / 256 CUs) (steps t + 1.2
-// us), t the time of one 128-code step: 256 x 256 1.25 us, 128 x 256 0.80,
-// 128 x 128 0.57, 128 x 64 0.51, 64 x 64 0.33.  With these the choice is the
-// fastest of the five tiles at each of the 42 shapes where all were timed (M
-// 32 to 8192; N, K 14336 x 4096, 8192 x 8192 and 2048 x 5120).
-Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, bool pipe) {
-    auto split = [&](int ms, int ns, int waves) {
-        return Form{Kind::kSplit, ms, ns,
-                    uint64_t(tile_bound(M, 16 * ms, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 64u * uint64_t(waves)};
+// Dense in whole pieces: with the times below the choice is the fastest of the
+// five tiles at each of the 42 shapes where all were timed (M 32 to 8192; N, K
+// 14336 x 4096, 8192 x 8192 and 2048 x 5120).
+//
+// Rows at any byte, dense [8191, 4095] and the same (us for tiles of 64 x 64, 128
+// x 64, 128 x 128, 128 x 256; the last form is 16 x 16 split):
+//   rows   64: 19.4 24.7 30.9 47.6 30.9    rows  512: 60.2 48.7 36.2 54.3 202
+//   rows  128: 20.3 24.6 32.1 51.7 55.2    rows 1024: 116  91.2 73.8 62.3 383
+//   rows  256: 31.9 26.3 33.0 52.2 109     rows 4096: 410  329  262  227
+// by expert, 64 of [2047, 5119]: rows 8 162, 188, 174, 158; 64 237, 248, 220,
+// 230; 256 608, 492, 430, 381.  Twice to three times those of whole pieces: the
+// loads of 16 bytes that straddle dwords take the address units as much longer.
+// Splitting the contraction wins while there are few workgroups of it, against
+// 64 x 64 tiles (us in a graph): dense, 16 x 16, 315 of them (77 x 1000 x 1111)
+// 4.8 and 6.9, 512 (64 x 2047 x 8191) 16.9 and 26.4, 1008 (256 x 1000 x 1041) 7.7
+// and 7.0, 1024 (64 x 4095 x 4095) 16.6 and 15.3; by expert, 16 x 32, 512 (8 of
+// [2047, 5119]) 19.4 and 25.3, 640 (64 of [301, 701]) 9.9 and 10.0, 1408 (64 of
+// [700, 513]) 15.6 and 11.9.
+Form choose(int64_t M, int64_t N, int64_t K, bool groups, int32_t G, Rows rows) {
+    auto split = [&](int ns) {
+        return Form{Kind::kSplit, 1, ns,
+                    uint64_t(tile_bound(M, 16, groups, G)) * uint64_t((N + 16 * ns - 1) / (16 * ns)) * 512u};
     };
-    const Form tiles{Kind::kTiles, 0, 0, uint64_t(tile_bound(M, kTile, groups, G)) * uint64_t((N + kTile - 1) / kTile) * 256};
-    auto piped = [&](int um, int un) {
+    auto tiled = [&](Kind kind, int um, int un) {
         const int64_t tm = tile_bound(M, 64 * um, groups, G), tn = (N + 64 * un - 1) / (64 * un);
-        return Form{Kind::kPipe, um, un, (groups ? uint64_t(group_tiles(tm)) * uint64_t(tn) : (uint64_t(tm) * uint64_t(tn) + 7) / 8 * 8) * 512};
+        return Form{kind, um, un, (groups ? uint64_t(group_tiles(tm)) * uint64_t(tn) : (uint64_t(tm) * uint64_t(tn) + 7) / 8 * 8) * 512};
     };
-    if (groups) {
-        const int64_t rows = (M + G - 1) / G;
-        if (pipe) return piped(rows <= 16 ? 1 : rows <= 160 ? 2 : 4, 4);
-        // rows that start at any byte, 64 of [2047, 5119] by 1, 8, 16, 24, 60 rows a
-        // group: 16 x 32 split 150, 186, 223, 267, 495 us, 128 x 128 tiles 225, 237,
-        // 239, 239, 317
-        return rows <= 18 ? split(1, 2, 8) : tiles;
-    }
-    if (pipe) {
+    const int64_t each = groups ? (M + G - 1) / G : M, parts = groups ? G : 1;   // rows of a group, groups
+    if (rows == Rows::kPieces) {
+        if (groups) return tiled(Kind::kPipe, each <= 16 ? 1 : each <= 160 ? 2 : 4, 4);
         if (M <= 16) return Form{Kind::kRing, 1, ring_columns(N), uint64_t((N + 15) / 16) * 512};
-        struct Tile {
-            int um, un;
-            double step;
-        };
         constexpr Tile kTiles[] = {{4, 4, 1.25}, {2, 4, 0.80}, {2, 2, 0.57}, {2, 1, 0.51}, {1, 1, 0.33}};
-        const Tile* best = nullptr;
-        double least = 0;
-        for (const Tile& t : kTiles) {
-            const int64_t n = ((M + 64 * t.um - 1) / (64 * t.um)) * ((N + 64 * t.un - 1) / (64 * t.un));
-            const double cost = double((n + 255) / 256) * (double((K + 127) / 128) * t.step + 1.2);
-            if (!best || cost < least) {
-                best = &t;
-                least = cost;
-            }
-        }
-        return piped(best->um, best->un);
+        const Tile& t = best_tile(kTiles, M, N, K, 1);
+        return tiled(Kind::kPipe, t.um, t.un);
     }
-    // rows that start at any byte, [8191, 4095] by 16, 64, 256, 512 rows: 16 x 16
-    // split 14.0, 35.2, 111.8, 209.9 us, 64 x 32 split 21.2, 21.5, 58.0, 102.9, 128 x
-    // 128 tiles 65.2, 70.2, 70.4, 70.7
-    if (((M + 15) / 16) * ((N + 15) / 16) <= 1024) return split(1, 1, 8);
-    return ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) < 192 ? split(4, 2, 4) : tiles;
+    if (groups ? parts * ((each + 15) / 16) * ((N + 31) / 32) <= 640 : ((M + 15) / 16) * ((N + 15) / 16) <= 768)
+        return split(groups ? 2 : 1);
+    if (rows == Rows::kFar) return split(2);
+    constexpr Tile kTiles[] = {{2, 4, 1.85}, {2, 2, 0.98}, {2, 1, 0.74}, {1, 1, 0.56}};
+    const Tile& t = best_tile(kTiles, each, N, K, parts);
+    return tiled(Kind::kStaged, t.um, t.un);
 }
 
 bool pipe_fits(const I8Args& p) {
     const auto aligned = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
     return aligned(p.A) && aligned(p.B) && p.lda % 16 == 0 && p.ldb % 16 == 0 && p.b_gs % 16 == 0 && p.K % 16 == 0 &&
-           p.K > 0 && p.lda < (1 << 23) && p.ldb < (1 << 23);
+           p.K > 0;
 }
 
 template <typename O>
 hipError_t launch(I8Args& p, hipStream_t stream) {
-    const Form f = choose(p.M, p.N, p.K, p.offs != nullptr, p.G, pipe_fits(p));
+    const Rows rows = far(p.lda, p.ldb) ? Rows::kFar : pipe_fits(p) ? Rows::kPieces : Rows::kBytes;
+    const Form f = choose(p.M, p.N, p.K, p.offs != nullptr, p.G, rows);
     if (f.kind == Kind::kRing) return ring<O, void>(p, stream);
     if (f.kind == Kind::kPipe) {
         // experts' weights pass through each L2 about once (measured: 113 us with
@@ -1108,20 +1123,23 @@ hipError_t launch(I8Args& p, hipStream_t stream) {
         if (f.ns == 2) return launch_pipe<O, 2, 4, 4, 2, 4, 4, false>(p, stream);
         return launch_pipe<O, 2, 2, 4, 2, 6, 6, false>(p, stream);
     }
-    if (f.kind == Kind::kTiles) return launch_tiles<O>(p, stream);
-    switch (f.ms * 8 + f.ns) {
-        case 8 + 1: return launch_split<O, 1, 1, 8>(p, stream);
-        case 8 + 2: return launch_split<O, 1, 2, 8>(p, stream);
-        default: return launch_split<O, 4, 2, 4>(p, stream);
+    if (f.kind == Kind::kStaged) {
+        if (f.ms == 1) return launch_staged<O, 1, 2, 4, 2>(p, stream);
+        if (f.ns == 1) return launch_staged<O, 2, 2, 4, 2>(p, stream);
+        if (f.ns == 2) return launch_staged<O, 2, 4, 4, 2>(p, stream);
+        return launch_staged<O, 4, 4, 2, 4>(p, stream);
     }
+    if (f.ns == 1) return launch_split<O, 1, 1, 8>(p, stream);
+    return launch_split<O, 1, 2, 8>(p, stream);
 }
 
 }  // namespace
 
 // The threads of the largest grid that a product of this shape launches.
-uint64_t i8_gemm_threads(int64_t M, int64_t N, int64_t K, bool groups, int32_t G) {
+uint64_t i8_gemm_threads(int64_t lda, int64_t ldb, int64_t M, int64_t N, int64_t K, bool groups, int32_t G) {
     if (M <= 0 || N <= 0) return 0;
-    const uint64_t a = choose(M, N, K, groups, G, false).threads, b = choose(M, N, K, groups, G, true).threads;
+    if (far(lda, ldb)) return choose(M, N, K, groups, G, Rows::kFar).threads;
+    const uint64_t a = choose(M, N, K, groups, G, Rows::kBytes).threads, b = choose(M, N, K, groups, G, Rows::kPieces).threads;
     return a > b ? a : b;
 }
 

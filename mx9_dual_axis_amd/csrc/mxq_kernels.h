@@ -105,7 +105,7 @@ hipError_t launch_combine_grad(const void* dy, int dtype, int64_t T, int64_t N, 
 
 // Product of 8-bit codes, C = A B^T with row scales (i8_gemm.hip); offs null:
 // dense.  M, N > 0, K <= 131071.
-uint64_t i8_gemm_threads(int64_t M, int64_t N, int64_t K, bool groups, int32_t G);
+uint64_t i8_gemm_threads(int64_t lda, int64_t ldb, int64_t M, int64_t N, int64_t K, bool groups, int32_t G);
 hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
                           const float* sB, int64_t sb_gs, const float* bias, void* C, int64_t ldc, int64_t M,
                           int64_t N, int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);

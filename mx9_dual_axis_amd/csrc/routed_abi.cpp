@@ -62,15 +62,17 @@ int quantize(const void* x, int32_t dtype, int64_t T, int64_t K, int64_t ld_x, c
     return status(mxq::launch_quantize_rows(x, dtype, T, K, ld_x, slot, src, k, M, q, ld_q, s, hip(stream)));
 }
 
-// Everything of a product but its left operand.
-int check_product(const int8_t* B, int64_t ldb, int64_t b_gs, const float* sB, int64_t sb_gs, const float* bias,
+int64_t code_pitch(int64_t K) { return (K + 15) / 16 * 16; }
+
+// Everything of a product but its left operand, whose rows are lda apart.
+int check_product(int64_t lda, const int8_t* B, int64_t ldb, int64_t b_gs, const float* sB, int64_t sb_gs, const float* bias,
                   const int32_t* offs, int32_t G, bool groups, int64_t M, int64_t N, int64_t K, const void* C,
                   int64_t ldc, int32_t out_dtype, Span* sp) {
     const bool some = M > 0 && N > 0;
     if (some && ((!B && K > 0) || !sB || !C || (groups && !offs))) return MX_E_NULL;
     if (!dtype_ok(out_dtype)) return MX_E_DTYPE;
     if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxCodes || G < 1) return MX_E_SHAPE;
-    if (mxq::i8_gemm_threads(M, N, K, groups, G) > kMaxThreads) return MX_E_SHAPE;
+    if (mxq::i8_gemm_threads(lda, ldb, M, N, K, groups, G) > kMaxThreads) return MX_E_SHAPE;
     if (ldb < K || ldc < N || b_gs < 0 || sb_gs < 0) return MX_E_STRIDE;
     const int64_t esz = elem(out_dtype);
     const uint64_t bb = matrix_bytes(N, K, ldb, 1), cb = matrix_bytes(M, N, ldc, esz);
@@ -91,7 +93,7 @@ int gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t
          int64_t K, void* C, int64_t ldc, int32_t out_dtype, void* stream) {
     if (M > 0 && N > 0 && ((!A && K > 0) || !sA)) return MX_E_NULL;
     Span sp[7];
-    int rc = check_product(B, ldb, b_gs, sB, sb_gs, bias, offs, G, groups, M, N, K, C, ldc, out_dtype, sp);
+    int rc = check_product(lda, B, ldb, b_gs, sB, sb_gs, bias, offs, G, groups, M, N, K, C, ldc, out_dtype, sp);
     if (rc != MX_OK) return rc;
     const uint64_t ab = matrix_bytes(M, K, lda, 1);
     if (lda < K || ab == kTooLarge) return MX_E_STRIDE;
@@ -103,8 +105,6 @@ int gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t
     return status(mxq::launch_i8_gemm(A, lda, sA, B, ldb, b_gs, sB, sb_gs, bias, C, ldc, M, N, K,
                                       groups ? offs : nullptr, groups ? G : 0, out_dtype, hip(stream)));
 }
-
-int64_t code_pitch(int64_t K) { return (K + 15) / 16 * 16; }
 
 }  // namespace
 
@@ -218,7 +218,7 @@ int i8_linear(const void* x, int32_t dtype, int64_t ld_x, const int8_t* B, int64
     if (some && ((!x && K > 0) || !workspace)) return MX_E_NULL;
     if (!dtype_ok(dtype)) return MX_E_DTYPE;
     Span sp[7];
-    int rc = check_product(B, ldb, 0, sB, 0, bias, nullptr, 1, false, M, N, K, C, ldc, out_dtype, sp);
+    int rc = check_product(code_pitch(K), B, ldb, 0, sB, 0, bias, nullptr, 1, false, M, N, K, C, ldc, out_dtype, sp);
     if (rc != MX_OK) return rc;
     const int64_t need = i8_linear_workspace(M, K);
     if (some && workspace_bytes < need) return MX_E_SHAPE;

@@ -157,6 +157,27 @@ def test_groups(sizes, tail, N, K, out):
     near(mxq.i8_grouped_gemm_rows(at_any_byte(a), sa, at_any_byte(b), sb, od, out_dtype=DT[out]), want, mag, DT[out], "any byte")
 
 
+# Rows so far apart that a tile's offsets leave 32 bits.
+@pytest.mark.parametrize("K", [64, 1041])
+@pytest.mark.parametrize("wide", ["A", "B"])
+def test_rows_far_apart(wide, K):
+    M, N, pitch = (130, 70, 2 ** 24 + 16) if wide == "A" else (70, 130, 2 ** 24 + 16)
+    g = gen(K)
+    a, b, sa, sb = codes((M, K), g), codes((N, K), g), scales(M, g), scales(N, g)
+    buf = torch.empty(130 * pitch, dtype=torch.int8, device=DEV)
+    v = buf.as_strided((130, K), (pitch, 1))
+    v.copy_(a if wide == "A" else b)
+    A, B = (v, b) if wide == "A" else (a, v)
+    want, mag = plain(a, sa, b, sb)
+    near(mxq.i8_gemm_nt(A, sa, B, sb), want, mag, torch.bfloat16, "dense")
+    ends = [0, 33, 34, M - 5]
+    offs = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    want, mag = plain(a, sa, b, sb)
+    want[M - 5:] = mag[M - 5:] = 0
+    got = mxq.i8_grouped_gemm_rows(A, sa, B.as_strided((4, N, K), (0, B.stride(0), 1)), sb.expand(4, N), offs)
+    near(got, want, mag, torch.bfloat16, "by expert")
+
+
 # -------------------------------------------------------------------- routing
 def plain_route(z, k, normalize, align, M):
     """Routing by sorts and sums in binary64 on the device (no invalid token,
