@@ -28,7 +28,8 @@
 //          the clock falls as the matrix cores fill), 64 experts of [2048, 5120]
 //          with 2 rows each 87 us (the weights' 580 MB), with 256 245 us.
 //   split  rows that start at any byte, few tiles: the waves of a workgroup
-//          split the contraction.  77 x 1000 x 1111: 5.2 us.
+//          split the contraction.  77 x 1000 x 1111: 4.8 us in a graph, 6.8
+//          with fp32 activations that it quantizes itself.
 //   staged rows that start at any byte, many tiles: as pipe, through registers.
 //          512 x 8191 x 4095: 36 us.
 #include "mxq_kernels.h"
@@ -227,7 +228,7 @@ __device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[MS]
         int64_t row, col;
         S::place(q, r, n0, &row, &col);
         if (row >= r.m1 || col >= p.N) continue;
-        float y = float(sum) * (sA ? sA[row] : share.sa[x]);
+        float y = float(sum) * (sA ? sA[row - r.m0] : share.sa[x]);
         y = p.bias ? __builtin_fmaf(y, share.sb[x], share.bias[x]) : y * share.sb[x];
         C[row * p.ldc + col] = Out<O>::get(zero ? 0.f : y);
     }
@@ -776,6 +777,7 @@ template <> struct Raw<float> {
     using T = float;
     static constexpr int kPer = 4;
     static __device__ __forceinline__ float get(const v4i& w, int e) { return __int_as_float(w[e]); }
+    static __device__ __forceinline__ float one(float x) { return x; }
 };
 template <> struct Raw<uint16_t> {
     using T = uint16_t;
@@ -783,6 +785,7 @@ template <> struct Raw<uint16_t> {
     static __device__ __forceinline__ float get(const v4i& w, int e) {
         return __uint_as_float(e & 1 ? uint32_t(w[e >> 1]) & 0xFFFF0000u : uint32_t(w[e >> 1]) << 16);
     }
+    static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
 };
 
 // A barrier that leaves loads on their way.
@@ -951,6 +954,153 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
     }
     __syncthreads();                                                         // every ring is read
     store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, kFuse ? scales : nullptr, false);
+}
+
+// ---- few tiles, activations quantized on the way ----
+//
+// The split form with float or bf16 activations (at any element) as its left
+// operand: a wave holds its two steps of 16 rows in registers, the waves'
+// largest magnitudes meet in LDS, and each quantizes what it holds.  A column
+// tile quantizes the rows anew; while that is little, it costs no more than a
+// kernel before the product, and a call saves a launch (fp32, us in a graph and
+// as a call, two kernels and this one: 77 x 1000 x 1111, 160 workgroups, 7.9,
+// 10.9 and 6.8, 8.7; 64 x 2047 x 2047, 256, 8.9, 11.5 and 9.1, 9.0; 300 x 600 x
+// 600, 361, 7.6, 11.5 and 6.8, 8.8; 128 x 1500 x 1023, 376, 7.9, 11.4 and 9.3,
+// 9.2; 250 x 770 x 2047, 400, 13.9, 14.0 and 14.3, 14.0).  16 columns a
+// workgroup instead of 32: 8.1, 12.1, 8.8, 11.6 and 20.6 in a graph.
+constexpr int64_t kFuseSplitCodes = 2048;                                   // two steps of 8 waves
+constexpr int64_t kFuseSplitTiles = 384;
+
+template <typename O, typename X>
+__global__ __launch_bounds__(512) void i8_split_fused_kernel(I8Args p) {
+    constexpr int NS = 2, kW = 8, kRows = 16 * (1 + NS), kPer = Raw<X>::kPer;
+    __shared__ v4i lds[kW * kRows * 8];
+    __shared__ uint32_t maxes[kW][16];
+    __shared__ float scales[16];
+    const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
+    const uint32_t wave = uint32_t(uniform(int32_t(threadIdx.x >> 6)));
+    const uint32_t tm = blockIdx.x % p.tiles_m, tn = blockIdx.x / p.tiles_m;
+    const RowTile r{int64_t(tm) * 16, p.M, 0};
+    const int64_t n0 = int64_t(tn) * (16 * NS);
+    const uint32_t K = uint32_t(p.K), lr = lane >> 3, piece = lane & 7u;
+    const uint32_t k0 = 128u * wave;
+    const X* rowx[2];
+    const int8_t* rowb[2 * NS];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        rowx[q] = reinterpret_cast<const X*>(p.A) + min(r.m0 + 8 * q + int64_t(lr), p.M - 1) * p.lda;
+#pragma unroll
+    for (int q = 0; q < 2 * NS; ++q) rowb[q] = p.B + min(n0 + 8 * q + int64_t(lr), p.N - 1) * p.ldb;
+
+    // x[h][q]: 16 of row 8 q + lr from 128 (wave + 8 h) + 16 piece, zeros past K
+    float x[2][2][16];
+    auto read_x = [&](uint32_t h) {
+        const uint32_t from = k0 + 1024u * h, k = from + 16u * piece;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (from + 128u <= K) {                                         // uniform
+                v4i w[16 / kPer];
+#pragma unroll
+                for (int c = 0; c < 16 / kPer; ++c) w[c] = load16(reinterpret_cast<const int8_t*>(rowx[q] + k + c * kPer));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[h][q][e] = Raw<X>::get(w[e / kPer], e % kPer);
+            } else {
+                X w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = rowx[q][min(k + e, K - 1u)];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[h][q][e] = k + e < K ? Raw<X>::one(w[e]) : 0.f;
+            }
+        }
+    };
+    v4i b[2][2 * NS];
+    auto read_b = [&](uint32_t h) {
+        const uint32_t from = k0 + 1024u * h;
+#pragma unroll
+        for (int q = 0; q < 2 * NS; ++q)
+            b[h][q] = from + 128u <= K ? load16(rowb[q] + from + 16u * piece) : load_codes(rowb[q], from + 16u * piece, K, K);
+    };
+    const bool first = k0 < K, second = k0 + 1024u < K;                     // uniform
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[h][q][e] = 0.f;
+    if (first) read_x(0);
+    if (second) read_x(1);
+    if (first) read_b(0);
+    if (second) read_b(1);
+    Share<1, NS, kW> share;
+    share.load(p, r, n0, wave, nullptr, p.sB);
+
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(x[h][q][e]) & 0x7FFFFFFFu);
+        m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0xB1, 0xF, 0xF, false)));    // quad_perm: lane ^ 1
+        m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x4E, 0xF, 0xF, false)));    // quad_perm: lane ^ 2
+        m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x141, 0xF, 0xF, false)));   // row_half_mirror
+        if (piece == 0) maxes[wave][8 * q + lr] = m;
+    }
+    lds_barrier();
+    v4i a[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) m = max(m, maxes[w][8 * q + lr]);
+        const float top = fmaxf(__uint_as_float(m), 127.f * 0x1p-126f);
+        const float inv = 127.f * (1.f / top);
+        const bool bad = m >= 0x7F800000u;
+        if (wave == 0 && piece == 0) scales[8 * q + lr] = bad ? __uint_as_float(0x7FC00000u) : top / 127.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v |= uint32_t(int(rintf(x[h][q][4 * c + e] * inv)) & 255) << (8 * e);
+                a[h][q][c] = bad ? 0 : int(v);
+            }
+    }
+
+    v4i* part = lds + wave * (kRows * 8);
+    const uint32_t at = lr * 8u + (piece ^ lr);
+    v4i acc[1][NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) acc[0][j] = v4i{0, 0, 0, 0};
+    auto step = [&](int h) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) part[64 * q + at] = a[h][q];
+#pragma unroll
+        for (int q = 0; q < 2 * NS; ++q) part[64 * (2 + q) + at] = b[h][q];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = (4u * i + g) ^ (l16 & 7u);
+            const v4i u = part[l16 * 8u + c];
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                acc[0][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(u, part[(16u * (1 + j) + l16) * 8u + c], acc[0][j], 0, 0, 0);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    if (first) step(0);
+    if (second) step(1);
+    __syncthreads();                                                       // every part is read
+    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, scales, false);
+}
+
+template <typename O, typename X>
+hipError_t launch_split_fused(I8Args& p, hipStream_t stream) {
+    p.tiles_m = uint32_t((p.M + 15) / 16);
+    p.tiles_n = uint32_t((p.N + 31) / 32);
+    hipLaunchKernelGGL((i8_split_fused_kernel<O, X>), dim3(p.tiles_m * p.tiles_n), dim3(512), 0, stream, p);
+    return hipGetLastError();
 }
 
 template <typename O, int NS, int kW, int kS, typename X>
@@ -1152,11 +1302,25 @@ hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const i
     return out_dtype == 0 ? launch<float>(p, stream) : launch<__bf16>(p, stream);
 }
 
-bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t K) {
-    const int64_t esz = dtype == 0 ? 4 : 2;
+namespace {
+
+bool ring_fuses(const void* x, int64_t esz, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t K) {
     return M <= 16 && K > 0 && K % 16 == 0 && M * K * esz <= kFuseBytes && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
            (M == 1 || ld_x * esz % 16 == 0) && (M - 1) * ld_x * esz < (1 << 30) && reinterpret_cast<uintptr_t>(B) % 16 == 0 &&
            ldb % 16 == 0 && ldb < (1 << 23);
+}
+
+template <typename X>
+hipError_t fused(I8Args& p, bool ring_fits, int out_dtype, hipStream_t stream) {
+    if (ring_fits) return out_dtype == 0 ? ring<float, X>(p, stream) : ring<__bf16, X>(p, stream);
+    return out_dtype == 0 ? launch_split_fused<float, X>(p, stream) : launch_split_fused<__bf16, X>(p, stream);
+}
+
+}  // namespace
+
+bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K) {
+    if (ring_fuses(x, dtype == 0 ? 4 : 2, ld_x, B, ldb, M, K)) return true;
+    return K > 0 && K <= kFuseSplitCodes && ((M + 15) / 16) * ((N + 31) / 32) <= kFuseSplitTiles;
 }
 
 hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, const float* sB,
@@ -1166,9 +1330,8 @@ hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const 
     p.A = static_cast<const int8_t*>(x); p.lda = ld_x; p.sA = nullptr; p.B = B; p.ldb = ldb; p.b_gs = 0; p.sB = sB;
     p.sb_gs = 0; p.bias = bias; p.C = C; p.ldc = ldc; p.M = M; p.N = N; p.K = K; p.offs = nullptr; p.G = 0;
     p.tiles_m = p.tiles_n = 0;
-    if (dtype == 0)
-        return out_dtype == 0 ? ring<float, float>(p, stream) : ring<__bf16, float>(p, stream);
-    return out_dtype == 0 ? ring<float, uint16_t>(p, stream) : ring<__bf16, uint16_t>(p, stream);
+    const bool ring_fits = ring_fuses(x, dtype == 0 ? 4 : 2, ld_x, B, ldb, M, K);
+    return dtype == 0 ? fused<float>(p, ring_fits, out_dtype, stream) : fused<uint16_t>(p, ring_fits, out_dtype, stream);
 }
 
 }  // namespace mxq

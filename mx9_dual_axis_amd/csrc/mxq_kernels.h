@@ -110,8 +110,8 @@ hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const i
                           const float* sB, int64_t sb_gs, const float* bias, void* C, int64_t ldc, int64_t M,
                           int64_t N, int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);
 // The product of activations that are quantized by the product's own kernel,
-// where i8_linear_fuses says so (few rows of whole 16-code pieces).
-bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t K);
+// where i8_linear_fuses says so (few rows of whole 16-code pieces, or few tiles).
+bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K);
 hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, const float* sB,
                                   const float* bias, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
                                   int out_dtype, hipStream_t stream);

@@ -234,7 +234,7 @@ int i8_linear(const void* x, int32_t dtype, int64_t ld_x, const int8_t* B, int64
     sp[4] = {addr(x), xb};
     if (outputs_clash(sp, 2, 6)) return MX_E_OVERLAP;
     if (!some) return MX_OK;
-    if (mxq::i8_linear_fuses(x, dtype, ld_x, B, ldb, M, K))
+    if (mxq::i8_linear_fuses(x, dtype, ld_x, B, ldb, M, N, K))
         return status(mxq::launch_i8_linear_fused(x, dtype, ld_x, B, ldb, sB, bias, C, ldc, M, N, K, out_dtype,
                                                   hip(stream)));
     int8_t* q = static_cast<int8_t*>(workspace);

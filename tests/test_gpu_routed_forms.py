@@ -124,6 +124,30 @@ def test_few_rows_of_activations(M, K, N, dtype):
             assert got[1:3].isnan().all() and not got[3].any()
 
 
+# Few tiles: activations quantized by the product itself up to 2048 of them, at
+# any element and pitch; beyond, and with more tiles, by a kernel before it.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (17, 40, 15), (20, 300, 128), (33, 70, 129), (77, 1000, 1111), (64, 500, 1024),
+                                   (5, 700, 1025), (100, 129, 2047), (40, 333, 2048), (40, 333, 2049), (300, 800, 600)])
+def test_rows_of_activations(M, N, K, dtype):
+    g = gen(M + N + K)
+    b, sb = at_any_byte(codes((N, K), g)), scales(N, g)
+    bias = torch.randn(N, generator=g, device=DEV)
+    buf = torch.full((M * (K + 3) + 8,), float("nan"), dtype=DT[dtype], device=DEV)
+    x = buf[1:1 + M * (K + 3)].view(M, K + 3)[:, :K]
+    x.copy_(torch.randn((M, K), generator=g, device=DEV) * scales((M, 1), g))
+    if M > 16:
+        x[1, K - 1] = float("nan")
+        x[16, K // 2] = float("inf")
+        x[3] = 0
+    q, s = ro.quantize(x.float().cpu().numpy())
+    qa, sa = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
+    for bi in (None, bias):
+        for out in (torch.float32, torch.bfloat16):
+            want, mag = plain(qa, sa, b, sb, bi)
+            near(mxq.i8_linear(x, b, sb, bi, out_dtype=out), want, mag.nan_to_num(0), out, str(out))
+
+
 # Rows that start at any byte: waves that split the contraction in 16 x 16 and
 # 64 x 32, and 128 x 128 tiles.
 @pytest.mark.parametrize("out", ["f32", "bf16"])
