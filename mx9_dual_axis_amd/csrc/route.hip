@@ -23,7 +23,7 @@
 // however many experts there are.  A bf16 score fits its key whole.  Of an
 // fp32 score 22 bits do; the picks are then checked by their scores, and where
 // those are out of order, or the last pick's 22 bits equal those of the score
-// after it, the four tokens of the wave are selected again by exact
+// after it (or a lane has given away all the keys it kept), the four tokens of the wave are selected again by exact
 // comparisons (about one wave in seven for scores spread like a normal
 // distribution over 256 experts).  Measured for 131072 tokens of 256 fp32
 // scores: exact maxima over all scores for each pick 86.6 us, sorted 64-bit
@@ -426,7 +426,10 @@ __global__ __launch_bounds__(kThr) void route_kernel(RouteArgs p) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 const float after = dpp<0x101>(score);                      // the next lane's (row_shl:1)
                 const uint32_t next = row_top(best[0]);
-                const bool wrong = (l16 + 1u < uint32_t(p.k) && score < after) || (KT::some(next) && KT::tied(last, next));
+                // a lane that won kKeep rounds has no key left (0 is none's) and may have
+                // dropped the score after the last pick
+                const bool wrong = (l16 + 1u < uint32_t(p.k) && score < after) || (KT::some(next) && KT::tied(last, next)) ||
+                                   (V > kKeep && best[0] == 0u);
                 if (__ballot(wrong) != 0) {                                 // uniform: the wave's four tokens
                     // the best score that comes after the last pick, k times
                     ok = false;

@@ -295,6 +295,27 @@ def test_scores_that_differ_in_their_last_bits(T, E, k, sign):
     check_route(zd, k, False, 1, 64 + -(-T // 64))
 
 
+# The best k + 1 scores of a row in one lane's experts, the last two of them
+# equal in their first 22 bits and out of the experts' order: a lane that keeps k
+# keys has dropped the one that shows it.
+@pytest.mark.parametrize("E,k,lane", [(256, 8, [0, 1, 2, 3, 64, 65, 66, 67, 128]), (512, 8, [4, 5, 6, 7, 68, 69, 70, 71, 132]),
+                                      (1024, 16, [b + i for b in (8, 72, 136, 200) for i in range(4)] + [264]),
+                                      (512, 16, [b + i for b in (8, 72, 136, 200) for i in range(4)] + [264]),
+                                      (1000, 8, [60, 61, 62, 63, 124, 125, 126, 127, 188])])
+def test_best_scores_in_one_lane(E, k, lane):
+    assert len(lane) == k + 1
+    z = np.full((70, E), -4.0, np.float32) - np.arange(E, dtype=np.float32) * 2.0 ** -10
+    g = np.random.default_rng(E)
+    for t in range(70):
+        order = g.permutation(k + 1)
+        low, high = min(order[-2:]), max(order[-2:])
+        for i, j in enumerate(order[:-2]):
+            z[t, lane[j]] = 8 - i * 0.25
+        z[t, lane[high]] = np.nextafter(np.float32(1), np.float32(2))      # the last pick: the later expert
+        z[t, lane[low]] = 1
+    check_route(torch.from_numpy(z).to(DEV), k, True, 1, 64 + 2)
+
+
 # More tokens than the gradient's grid takes at once (4096 workgroups of 16).
 @pytest.mark.parametrize("normalize", [True, False])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
