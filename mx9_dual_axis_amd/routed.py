@@ -67,13 +67,12 @@ _device = torch._C._cuda_getDevice
 _stream = torch._C._cuda_getCurrentRawStream
 
 
-def _run(dev, f, *args):
-    """Call an entry point on `dev`'s current stream and raise on a status."""
-    i = dev.index
+def _run(i, f, *args):
+    """Call an entry point on device i's current stream and raise on a status."""
     if i == _device():
         rc = f(*args, _stream(i))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(i):
             rc = f(*args, _stream(i))
     if rc:
         from . import MXError, status_string
@@ -83,61 +82,62 @@ def _run(dev, f, *args):
 
 # The checks below answer for a good argument at once; what is wrong with a bad
 # one is found out apart, since the smallest calls last as long as their checks.
-def _matrix(t, name, dtypes, dev=None):
-    """A 2-d device tensor with contiguous rows; returns its row pitch."""
+# Devices go by index: -1 is the host.
+def _matrix(t, name, dtypes, i=None):
+    """(row pitch, rows, cols) of a 2-d device tensor with contiguous rows."""
     try:
         rows, cols = t.shape
         pitch, step = t.stride()
-        if t.is_cuda and t.dtype in dtypes and (step == 1 or cols <= 1) and (dev is None or t.device == dev):
+        on = t.get_device()
+        if (on == i if i is not None else on >= 0) and t.dtype in dtypes and (step == 1 or cols <= 1):
             if pitch >= cols:
-                return pitch
+                return pitch, rows, cols
             if rows <= 1:
-                return cols
+                return cols, rows, cols
     except (AttributeError, TypeError, ValueError):
         pass
-    _bad_matrix(t, name, dtypes, dev)
+    _bad_matrix(t, name, dtypes, i)
 
 
-def _bad_matrix(t, name, dtypes, dev):
+def _bad_matrix(t, name, dtypes, i):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, not {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, not {tuple(t.shape)}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+    if i is not None and t.get_device() != i:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{i}")
     if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
     raise ValueError(f"the rows of {name} must not overlap")
 
 
-def _flat(t, name, dtype, shape, dev):
+def _flat(t, name, dtype, shape, i):
     """A contiguous device tensor of one dtype and shape; returns its pointer."""
     if isinstance(t, torch.Tensor):
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == i:
             return t.data_ptr()
-        if t.dtype is dtype and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+        if t.dtype is dtype and t.get_device() != i:
+            raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{i}")
         if t.dtype is dtype:
             raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
     raise ValueError(f"{name} must be a {dtype} tensor")
 
 
-def _valid(valid, T, dev):
+def _valid(valid, T, i):
     if valid is None:
         return None
     if valid.dtype is torch.bool:
-        return _flat(valid, "valid", torch.bool, (T,), dev)
-    return _flat(valid, "valid", torch.uint8, (T,), dev)
+        return _flat(valid, "valid", torch.bool, (T,), i)
+    return _flat(valid, "valid", torch.uint8, (T,), i)
 
 
 def _out_matrix(out, name, shape, dtype, like):
     """`out`, or a new matrix on the device of `like`; and its row pitch."""
-    dev = like.device
     if out is None:
         return like.new_empty(shape, dtype=dtype), shape[1]
-    pitch = _matrix(out, name, (dtype,), dev)
+    pitch = _matrix(out, name, (dtype,), like.get_device())[0]
     if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(out.shape)}")
     return out, pitch
@@ -199,19 +199,17 @@ def mx_route(logits: torch.Tensor, k: int | None = None, valid: torch.Tensor | N
     `normalize`; counts, offs, slot and src describe the padded buffer that
     the grouped casts and products take; loss is the balance loss.  With out (an
     MXRouting) k and align are those it was made for."""
-    ld = _matrix(logits, "logits", _ESZ)
-    T, E = logits.shape
-    dev = logits.device
+    ld, T, E = _matrix(logits, "logits", _ESZ)
+    i = logits.get_device()
     if out is None:
         if k is None:
             raise ValueError("k is needed when out is not given")
-        out = MXRouting(T, E, k, align, dev)
-    elif out.T != T or out.E != E or out.device != dev or (k is not None and k != out.k):
+        out = MXRouting(T, E, k, align, logits.device)
+    elif out.T != T or out.E != E or out.device.index != i or (k is not None and k != out.k):
         raise ValueError(f"out was made for T={out.T}, E={out.E}, k={out.k} on {out.device}, the call has T={T}, "
-                         f"E={E}, k={k} on {dev}")
-    p = out._ptrs
-    _run(dev, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, dev), out.k,
-         1 if normalize else 0, out.align, out.rows, *p)
+                         f"E={E}, k={k} on {logits.device}")
+    _run(i, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), out.k,
+         1 if normalize else 0, out.align, out.rows, *out._ptrs)
     out.normalize = bool(normalize)
     return out
 
@@ -221,46 +219,52 @@ def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tenso
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of the routing's weight (dweight float32 [T, k]) and loss
     (dloss float32 [1]) with respect to the logits, in their dtype."""
-    ld = _matrix(logits, "logits", _ESZ)
-    T, E = logits.shape
-    dev = logits.device
-    if routing.T != T or routing.E != E or routing.device != dev:
+    ld, T, E = _matrix(logits, "logits", _ESZ)
+    i = logits.get_device()
+    if routing.T != T or routing.E != E or routing.device.index != i:
         raise ValueError("routing was made for other logits")
-    dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), dev)
-    dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), dev)
+    dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), i)
+    dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), i)
     out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, logits)
     p = routing._ptrs
-    _run(dev, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, dev), routing.k,
+    _run(i, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), routing.k,
          1 if routing.normalize else 0, p[0], p[1], dw, p[4], p[6], dl, out.data_ptr(), ld_d)
     return out
 
 
-def _slots(slot, dev):
-    if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
-        raise ValueError("slot must be an int32 [T, k] tensor")
-    shape = slot.shape
-    return _flat(slot, "slot", _I32, shape, dev), shape[0], shape[1]
+def _slots(slot, i):
+    """(pointer, T, k)"""
+    try:
+        T, k = slot.shape
+        if slot.dtype is _I32 and slot.is_contiguous() and slot.get_device() == i:
+            return slot.data_ptr(), T, k
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("slot must be an int32 [T, k] tensor") from None
+    return _flat(slot, "slot", _I32, (T, k), i), T, k
 
 
-def _src(src, dev):
-    if not isinstance(src, torch.Tensor) or src.dim() != 1:
-        raise ValueError("src must be an int32 [M] tensor")
-    shape = src.shape
-    return _flat(src, "src", _I32, shape, dev), shape[0]
+def _src(src, i):
+    """(pointer, M)"""
+    try:
+        (M,) = src.shape
+        if src.dtype is _I32 and src.is_contiguous() and src.get_device() == i:
+            return src.data_ptr(), M
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("src must be an int32 [M] tensor") from None
+    return _flat(src, "src", _I32, (M,), i), M
 
 
 def mx_dispatch(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out: torch.Tensor | None = None):
     """Rows of the padded buffer: x[t] at slot[t, j] for every pick, 0 where
     src is -1.  x is float32 or bfloat16 [T, N] with rows at any pitch."""
-    ld = _matrix(x, "x", _ESZ)
-    dev = x.device
-    sp, T, k = _slots(slot, dev)
-    rp, M = _src(src, dev)
-    if T != x.shape[0]:
-        raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
-    N = x.shape[1]
+    ld, rows, N = _matrix(x, "x", _ESZ)
+    i = x.get_device()
+    sp, T, k = _slots(slot, i)
+    rp, M = _src(src, i)
+    if T != rows:
+        raise ValueError(f"slot has {T} tokens, x {rows}")
     out, ld_o = _out_matrix(out, "out", (M, N), x.dtype, x)
-    _run(dev, _L().mx_dispatch, x.data_ptr(), _ESZ[x.dtype], T, N, ld, sp, rp, k, M, out.data_ptr(), ld_o)
+    _run(i, _L().mx_dispatch, x.data_ptr(), _ESZ[x.dtype], T, N, ld, sp, rp, k, M, out.data_ptr(), ld_o)
     return out
 
 
@@ -275,36 +279,34 @@ def _codes_out(out, rows, K, like):
     if q is None:
         raise ValueError("out must be two tensors, the codes and the scales")
     q, pitch = _out_matrix(q, "out[0]", (rows, K), _I8, like)
-    _flat(s, "out[1]", _F32, (rows,), like.device)
+    _flat(s, "out[1]", _F32, (rows,), like.get_device())
     return q, pitch, s
 
 
 def mx_dispatch_i8(x: torch.Tensor, slot: torch.Tensor, src: torch.Tensor, out=None):
     """mx_dispatch with each row quantized: (q int8 [M, K], s float32 [M])."""
-    ld = _matrix(x, "x", _ESZ)
-    dev = x.device
-    sp, T, k = _slots(slot, dev)
-    rp, M = _src(src, dev)
-    if T != x.shape[0]:
-        raise ValueError(f"slot has {T} tokens, x {x.shape[0]}")
-    K = x.shape[1]
+    ld, rows, K = _matrix(x, "x", _ESZ)
+    i = x.get_device()
+    sp, T, k = _slots(slot, i)
+    rp, M = _src(src, i)
+    if T != rows:
+        raise ValueError(f"slot has {T} tokens, x {rows}")
     q, pitch, s = _codes_out(out, M, K, x)
-    _run(dev, _L().mx_dispatch_i8, x.data_ptr(), _ESZ[x.dtype], T, K, ld, sp, rp, k, M, q.data_ptr(), pitch,
+    _run(i, _L().mx_dispatch_i8, x.data_ptr(), _ESZ[x.dtype], T, K, ld, sp, rp, k, M, q.data_ptr(), pitch,
          s.data_ptr())
     return q, s
 
 
 def i8_quantize_rows(x: torch.Tensor, out=None):
     """(q int8 [T, K], s float32 [T]): x[t] ~ q[t] s[t], s = max |x[t]| / 127."""
-    ld = _matrix(x, "x", _ESZ)
-    T, K = x.shape
+    ld, T, K = _matrix(x, "x", _ESZ)
     q, pitch, s = _codes_out(out, T, K, x)
-    _run(x.device, _L().i8_quantize_rows, x.data_ptr(), _ESZ[x.dtype], T, K, ld, q.data_ptr(), pitch, s.data_ptr())
+    _run(x.get_device(), _L().i8_quantize_rows, x.data_ptr(), _ESZ[x.dtype], T, K, ld, q.data_ptr(), pitch, s.data_ptr())
     return q, s
 
 
-def _bias(bias, N, dev):
-    return None if bias is None else _flat(bias, "bias", _F32, (N,), dev)
+def _bias(bias, N, i):
+    return None if bias is None else _flat(bias, "bias", _F32, (N,), i)
 
 
 def _product_out(out, shape, out_dtype, like):
@@ -321,16 +323,14 @@ def i8_gemm_nt(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Ten
                bias: torch.Tensor | None = None, out_dtype=torch.bfloat16, out: torch.Tensor | None = None):
     """C = A B^T: int8 codes A [M, K] and B [N, K] (rows at any pitch), float32
     scales sA [M] and sB [N], optional float32 bias [N]."""
-    lda = _matrix(A, "A", (_I8,))
-    dev = A.device
-    ldb = _matrix(B, "B", (_I8,), dev)
-    M, K = A.shape
-    N = B.shape[0]
-    if B.shape[1] != K:
+    lda, M, K = _matrix(A, "A", (_I8,))
+    i = A.get_device()
+    ldb, N, KB = _matrix(B, "B", (_I8,), i)
+    if KB != K:
         raise ValueError("A and B must share the contraction extent")
-    sa, sb, bi = _flat(sA, "sA", _F32, (M,), dev), _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
+    sa, sb, bi = _flat(sA, "sA", _F32, (M,), i), _flat(sB, "sB", _F32, (N,), i), _bias(bias, N, i)
     out, ldc = _product_out(out, (M, N), out_dtype, A)
-    _run(dev, _L().i8_gemm_nt, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
+    _run(i, _L().i8_gemm_nt, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
          _ESZ[out.dtype])
     return out
 
@@ -339,18 +339,16 @@ def i8_linear(x: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, bias: torch.Te
               out: torch.Tensor | None = None):
     """i8_quantize_rows of x [M, K] and i8_gemm_nt in one call; the result has
     x's dtype unless out_dtype or out says otherwise."""
-    ld = _matrix(x, "x", _ESZ)
-    dev = x.device
-    ldb = _matrix(B, "B", (_I8,), dev)
-    M, K = x.shape
-    N = B.shape[0]
-    if B.shape[1] != K:
+    ld, M, K = _matrix(x, "x", _ESZ)
+    i = x.get_device()
+    ldb, N, KB = _matrix(B, "B", (_I8,), i)
+    if KB != K:
         raise ValueError("x and B must share the contraction extent")
-    sb, bi = _flat(sB, "sB", _F32, (N,), dev), _bias(bias, N, dev)
+    sb, bi = _flat(sB, "sB", _F32, (N,), i), _bias(bias, N, i)
     out, ldc = _product_out(out, (M, N), out_dtype or x.dtype, x)
     size = M * ((K + 15) // 16 * 16) + (M * 4 + 15) // 16 * 16
     ws = x.new_empty((size,), dtype=torch.uint8)
-    _run(dev, _L().i8_linear, x.data_ptr(), _ESZ[x.dtype], ld, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
+    _run(i, _L().i8_linear, x.data_ptr(), _ESZ[x.dtype], ld, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
          _ESZ[out.dtype], ws.data_ptr(), size)
     return out
 
@@ -360,23 +358,23 @@ def i8_grouped_gemm_rows(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB:
     """Rows of group g (cumulative int32 ends offs [G], groups of any size) with
     expert g's codes B[g] ([E, N, K], E >= G) and scales sB[g] ([E, N]); rows
     from offs[-1] on give 0."""
-    lda = _matrix(A, "A", (_I8,))
-    dev = A.device
-    M, K = A.shape
-    if not isinstance(B, torch.Tensor) or B.dtype is not _I8 or B.dim() != 3 or B.device != dev:
+    lda, M, K = _matrix(A, "A", (_I8,))
+    i = A.get_device()
+    if not isinstance(B, torch.Tensor) or B.dtype is not _I8 or B.dim() != 3 or B.get_device() != i:
         raise ValueError("B must be int8 [E, N, K] codes on the device of A")
-    E, N = B.shape[0], B.shape[1]
-    if B.shape[2] != K or (K > 1 and B.stride(2) != 1) or (N > 1 and B.stride(1) < K):
+    E, N, KB = B.shape
+    b_gs, ldb, step = B.stride()
+    if KB != K or (K > 1 and step != 1) or (N > 1 and ldb < K):
         raise ValueError("B must be [E, N, K] codes with contiguous rows that share A's contraction extent")
-    if not isinstance(sB, torch.Tensor) or sB.dtype is not _F32 or sB.shape != (E, N) or sB.device != dev or (
+    if not isinstance(sB, torch.Tensor) or sB.dtype is not _F32 or sB.shape != (E, N) or sB.get_device() != i or (
             N > 1 and sB.stride(1) != 1):
         raise ValueError("sB must be a float32 [E, N] tensor with contiguous rows")
     if not isinstance(offs, torch.Tensor) or offs.dim() != 1 or not 1 <= offs.shape[0] <= E:
         raise ValueError("offs must be an int32 [G] tensor with 1 <= G <= E")
     G = offs.shape[0]
-    sa, of = _flat(sA, "sA", _F32, (M,), dev), _flat(offs, "offs", _I32, (G,), dev)
+    sa, of = _flat(sA, "sA", _F32, (M,), i), _flat(offs, "offs", _I32, (G,), i)
     out, ldc = _product_out(out, (M, N), out_dtype, A)
-    _run(dev, _L().i8_grouped_gemm_rows, A.data_ptr(), lda, sa, B.data_ptr(), max(B.stride(1), K), B.stride(0),
+    _run(i, _L().i8_grouped_gemm_rows, A.data_ptr(), lda, sa, B.data_ptr(), ldb if ldb > K else K, b_gs,
          sB.data_ptr(), sB.stride(0), of, G, M, N, K, out.data_ptr(), ldc, _ESZ[out.dtype])
     return out
 
@@ -385,13 +383,12 @@ def mx_combine(rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor | No
                out: torch.Tensor | None = None):
     """y[t] = sum_j weight[t, j] rows[slot[t, j]] (weight None: 1) over the
     picks that have a slot."""
-    ld = _matrix(rows, "rows", _ESZ)
-    dev = rows.device
-    sp, T, k = _slots(slot, dev)
-    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
-    M, N = rows.shape
+    ld, M, N = _matrix(rows, "rows", _ESZ)
+    i = rows.get_device()
+    sp, T, k = _slots(slot, i)
+    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), i)
     out, ld_y = _out_matrix(out, "out", (T, N), rows.dtype, rows)
-    _run(dev, _L().mx_combine, rows.data_ptr(), _ESZ[rows.dtype], M, N, ld, sp, wp, k, T, out.data_ptr(), ld_y)
+    _run(i, _L().mx_combine, rows.data_ptr(), _ESZ[rows.dtype], M, N, ld, sp, wp, k, T, out.data_ptr(), ld_y)
     return out
 
 
@@ -400,20 +397,19 @@ def mx_combine_grad(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, we
     """(drows, dweight) of mx_combine for dy [T, N]: drows[slot[t, j]] =
     weight[t, j] dy[t], 0 where src is -1; dweight[t, j] = <dy[t],
     rows[slot[t, j]]>."""
-    ld_g = _matrix(dy, "dy", _ESZ)
-    dev = dy.device
-    ld_r = _matrix(rows, "rows", (dy.dtype,), dev)
-    sp, T, k = _slots(slot, dev)
-    rp, M = _src(src, dev)
-    N = dy.shape[1]
-    if dy.shape[0] != T or rows.shape != (M, N):
+    ld_g, tokens, N = _matrix(dy, "dy", _ESZ)
+    i = dy.get_device()
+    ld_r = _matrix(rows, "rows", (dy.dtype,), i)[0]
+    sp, T, k = _slots(slot, i)
+    rp, M = _src(src, i)
+    if tokens != T or rows.shape != (M, N):
         raise ValueError(f"dy must be [{T}, N] and rows [{M}, N], not {tuple(dy.shape)} and {tuple(rows.shape)}")
-    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), dev)
+    wp = None if weight is None else _flat(weight, "weight", _F32, (T, k), i)
     drows, dweight = out if out is not None else (None, None)
     drows, ld_d = _out_matrix(drows, "out[0]", (M, N), dy.dtype, dy)
     if dweight is None:
         dweight = dy.new_empty((T, k), dtype=_F32)
-    dp = _flat(dweight, "out[1]", _F32, (T, k), dev)
-    _run(dev, _L().mx_combine_grad, dy.data_ptr(), _ESZ[dy.dtype], T, N, ld_g, rows.data_ptr(), ld_r, sp, wp, rp, k, M,
+    dp = _flat(dweight, "out[1]", _F32, (T, k), i)
+    _run(i, _L().mx_combine_grad, dy.data_ptr(), _ESZ[dy.dtype], T, N, ld_g, rows.data_ptr(), ld_r, sp, wp, rp, k, M,
          drows.data_ptr(), ld_d, dp)
     return drows, dweight
