@@ -185,7 +185,10 @@ class MXRouting:
 
 def mx_routing(T: int, E: int, k: int, align: int = 128, device="cuda") -> MXRouting:
     """The buffers of mx_route for T tokens, E experts and k picks each, groups
-    padded to multiples of `align` (128 for the MXFP8 grouped calls)."""
+    padded to multiples of `align` (128 for the MXFP8 grouped calls).  Each
+    mx_route writes them anew: streams that run at once need a routing each, and
+    one that is used on another stream than it was made on is kept until that
+    work is done, as any tensor."""
     return MXRouting(T, E, k, align, device)
 
 
