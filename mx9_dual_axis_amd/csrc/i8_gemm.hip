@@ -167,25 +167,26 @@ template <> struct Out<__bf16> {
 
 // ---- few tiles, any alignment: every wave for itself ----
 //
-// One workgroup of kW waves computes (16 MS) x (16 NS) of C.  Wave w takes the
+// One workgroup of kW waves computes 16 x (16 NS) of C.  Wave w takes the
 // steps (128 codes) w, w + kW, ... of the contraction: it loads eight lanes to
 // a row, 16 bytes each, lays the pieces out in its own part of LDS (next
 // step's loads under way), and multiplies; the waves' integer sums meet at the
 // end.  (Loading fragments straight into registers, sixteen rows at a time,
 // touched four times as many cache lines per load: 77 x 1000 x 1111 took 8.8
 // us, 5.2 so.)
+
 // What a wave multiplies its share of a workgroup's sums by: accumulators
-// wave, wave + kW, ... of the (16 MS) x (16 NS) tile.  Read before the
-// contraction, whose loads hide theirs.
-template <int MS, int NS, int kW>
+// wave, wave + kW, ... of the 16 x (16 NS) tile.  Read before the contraction,
+// whose loads hide theirs.
+template <int NS, int kW>
 struct Share {
-    static constexpr int kRegs = MS * NS * 4, kN = (kRegs + kW - 1) / kW;
+    static constexpr int kRegs = NS * 4, kN = (kRegs + kW - 1) / kW;
     float sa[kN], sb[kN], bias[kN];
 
     static __device__ __forceinline__ void place(uint32_t q, const RowTile& r, int64_t n0, int64_t* row, int64_t* col) {
-        const uint32_t lane = threadIdx.x & 63u, i = q / (4 * NS), j = q / 4 % NS, v = q & 3u;
-        *row = r.m0 + 16 * i + 4 * (lane >> 4) + v;
-        *col = n0 + 16 * j + (lane & 15u);
+        const uint32_t lane = threadIdx.x & 63u;
+        *row = r.m0 + 4 * (lane >> 4) + (q & 3u);
+        *col = n0 + 16 * (q >> 2) + (lane & 15u);
     }
     __device__ __forceinline__ void load(const I8Args& p, const RowTile& r, int64_t n0, uint32_t wave, const float* sA,
                                          const float* sB) {
@@ -204,18 +205,15 @@ struct Share {
 
 // The sums of a workgroup's waves, which split the contraction, meet in LDS
 // and become C's tile.  sA: in LDS, or null where the share has them.
-template <typename O, int MS, int NS, int kW>
-__device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[MS][NS], int* sums, const RowTile& r,
-                                           int64_t n0, uint32_t wave, const Share<MS, NS, kW>& share, const float* sA,
-                                           bool zero) {
-    using S = Share<MS, NS, kW>;
+template <typename O, int NS, int kW>
+__device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[NS], int* sums, const RowTile& r, int64_t n0,
+                                           uint32_t wave, const Share<NS, kW>& share, const float* sA, bool zero) {
+    using S = Share<NS, kW>;
     const uint32_t lane = threadIdx.x & 63u;
 #pragma unroll
-    for (int i = 0; i < MS; ++i)
+    for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) sums[(wave * S::kRegs + (i * NS + j) * 4 + v) * 64 + lane] = acc[i][j][v];
+        for (int v = 0; v < 4; ++v) sums[(wave * S::kRegs + j * 4 + v) * 64 + lane] = acc[j][v];
     __syncthreads();
     O* C = static_cast<O*>(p.C);
 #pragma unroll
@@ -234,22 +232,22 @@ __device__ __forceinline__ void store_sums(const I8Args& p, const v4i (&acc)[MS]
     }
 }
 
-template <typename O, int MS, int NS, int kW>
+template <typename O, int NS, int kW>
 __global__ __launch_bounds__(64 * kW) void i8_split_kernel(I8Args p) {
-    constexpr int kRows = 16 * (MS + NS), kLA = 2 * MS, kL = 2 * (MS + NS);
-    static_assert(kRows * 8 * 4 >= MS * NS * 4 * 64, "the sums take a wave's part of LDS");
+    constexpr int kRows = 16 * (1 + NS), kLA = 2, kL = 2 * (1 + NS);
+    static_assert(kRows * 8 * 4 >= NS * 4 * 64, "the sums take a wave's part of LDS");
     __shared__ v4i lds[kW * kRows * 8];
     const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, g = lane >> 4;
     const uint32_t wave = uint32_t(uniform(int32_t(threadIdx.x >> 6)));
     const uint32_t tm = p.offs ? blockIdx.x / p.tiles_n : blockIdx.x % p.tiles_m;
     const uint32_t tn = p.offs ? blockIdx.x - tm * p.tiles_n : blockIdx.x / p.tiles_m;
     RowTile r;
-    if (!find_tile<16 * MS>(p.offs, p.G, p.M, tm, &r)) return;             // uniform
+    if (!find_tile<16>(p.offs, p.G, p.M, tm, &r)) return;                  // uniform
     const int64_t n0 = int64_t(tn) * (16 * NS);
     const bool zero = p.offs != nullptr && r.g >= p.G;
     const int8_t* B = p.B + (zero ? 0 : int64_t(r.g) * p.b_gs);
     const float* sB = p.sB + (zero ? 0 : int64_t(r.g) * p.sb_gs);
-    Share<MS, NS, kW> share;
+    Share<NS, kW> share;
     share.load(p, r, n0, wave, p.sA, sB);
 
     // load q brings rows 8 q .. 8 q + 7 of A's tile, then of B's; rows past the end repeat the last
@@ -272,11 +270,9 @@ __global__ __launch_bounds__(64 * kW) void i8_split_kernel(I8Args p) {
             for (int q = 0; q < kL; ++q) v[q] = load_codes(from[q], k + 16 * piece, p.K, p.K);
         }
     };
-    v4i acc[MS][NS];
+    v4i acc[NS];
 #pragma unroll
-    for (int i = 0; i < MS; ++i)
-#pragma unroll
-        for (int j = 0; j < NS; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    for (int j = 0; j < NS; ++j) acc[j] = v4i{0, 0, 0, 0};
     int64_t k = zero ? p.K : 128 * int64_t(wave);
     if (k < p.K) load(k);
     for (; k < p.K; k += 128 * kW) {
@@ -287,21 +283,17 @@ __global__ __launch_bounds__(64 * kW) void i8_split_kernel(I8Args p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t c = (4u * h + g) ^ (l16 & 7u);
-            v4i a[MS], b[NS];
+            const v4i a = part[l16 * 8u + c];
+            v4i b[NS];
 #pragma unroll
-            for (int i = 0; i < MS; ++i) a[i] = part[(16u * i + l16) * 8u + c];
+            for (int j = 0; j < NS; ++j) b[j] = part[(16u * (1 + j) + l16) * 8u + c];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) b[j] = part[(16u * (MS + j) + l16) * 8u + c];
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < NS; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[j], acc[j], 0, 0, 0);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     __syncthreads();                                                       // every part is read
-    store_sums<O, MS, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, nullptr, zero);
+    store_sums<O, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, nullptr, zero);
 }
 
 // ---- many tiles, aligned operands: pipelined through LDS ----
@@ -906,7 +898,7 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
         for (uint32_t i = 0; i < uint32_t(kS); ++i)
             if (i < mine) issue(i, i);
     };
-    Share<1, NS, kW> share;
+    Share<NS, kW> share;
     share.load(p, r, n0, wave, kFuse ? nullptr : p.sA, p.sB);
     const uint32_t pitch = (K + 127u) / 128u * 128u + 16u;
     uint8_t* codes = lds + kRing;
@@ -919,9 +911,9 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
         fill();
     }
 
-    v4i acc[1][NS];
+    v4i acc[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) acc[0][j] = v4i{0, 0, 0, 0};
+    for (int j = 0; j < NS; ++j) acc[j] = v4i{0, 0, 0, 0};
     uint32_t slot = 0;
     for (uint32_t i = 0; i < mine; ++i) {
         // step i has arrived; near the end, where fewer are under way, all are waited for
@@ -943,7 +935,7 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 const v4i b = reinterpret_cast<const v4i*>(at)[(16u * j + l16) * 8u + (piece ^ (l16 & 7u))];
-                acc[0][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc[0][j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc[j], 0, 0, 0);
             }
         }
         if (i + kS < mine) {
@@ -953,7 +945,7 @@ __global__ __launch_bounds__(64 * kW) void i8_ring_kernel(I8Args p) {
         slot = slot + 1u == uint32_t(kS) ? 0u : slot + 1u;
     }
     __syncthreads();                                                         // every ring is read
-    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, kFuse ? scales : nullptr, false);
+    store_sums<O, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, kFuse ? scales : nullptr, false);
 }
 
 // ---- few tiles, activations quantized on the way ----
@@ -1031,7 +1023,7 @@ __global__ __launch_bounds__(512) void i8_split_fused_kernel(I8Args p) {
     if (second) read_x(1);
     if (first) read_b(0);
     if (second) read_b(1);
-    Share<1, NS, kW> share;
+    Share<NS, kW> share;
     share.load(p, r, n0, wave, nullptr, p.sB);
 
 #pragma unroll
@@ -1070,9 +1062,9 @@ __global__ __launch_bounds__(512) void i8_split_fused_kernel(I8Args p) {
 
     v4i* part = lds + wave * (kRows * 8);
     const uint32_t at = lr * 8u + (piece ^ lr);
-    v4i acc[1][NS];
+    v4i acc[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) acc[0][j] = v4i{0, 0, 0, 0};
+    for (int j = 0; j < NS; ++j) acc[j] = v4i{0, 0, 0, 0};
     auto step = [&](int h) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) part[64 * q + at] = a[h][q];
@@ -1085,14 +1077,14 @@ __global__ __launch_bounds__(512) void i8_split_fused_kernel(I8Args p) {
             const v4i u = part[l16 * 8u + c];
 #pragma unroll
             for (int j = 0; j < NS; ++j)
-                acc[0][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(u, part[(16u * (1 + j) + l16) * 8u + c], acc[0][j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(u, part[(16u * (1 + j) + l16) * 8u + c], acc[j], 0, 0, 0);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     if (first) step(0);
     if (second) step(1);
     __syncthreads();                                                       // every part is read
-    store_sums<O, 1, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, scales, false);
+    store_sums<O, NS, kW>(p, acc, reinterpret_cast<int*>(lds), r, n0, wave, share, scales, false);
 }
 
 template <typename O, typename X>
@@ -1137,12 +1129,12 @@ hipError_t launch_staged(I8Args& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename O, int MS, int NS, int kW>
+template <typename O, int NS, int kW>
 hipError_t launch_split(I8Args& p, hipStream_t stream) {
-    p.tiles_m = uint32_t(tile_bound(p.M, 16 * MS, p.offs != nullptr, p.G));
+    p.tiles_m = uint32_t(tile_bound(p.M, 16, p.offs != nullptr, p.G));
     p.tiles_n = uint32_t((p.N + 16 * NS - 1) / (16 * NS));
     const dim3 grid(p.tiles_m * p.tiles_n), block(64 * kW);
-    hipLaunchKernelGGL((i8_split_kernel<O, MS, NS, kW>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((i8_split_kernel<O, NS, kW>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1164,7 +1156,7 @@ hipError_t ring(I8Args& p, hipStream_t stream) {
 enum class Kind { kSplit, kStaged, kRing, kPipe };
 struct Form {
     Kind kind;
-    int ms, ns;                  // kSplit: 16-row, 16-column sub-tiles of a workgroup; kStaged, kPipe: 64-row, 64-column units
+    int ms, ns;                  // kSplit, kRing: 16 rows and 16-column parts of a workgroup; kStaged, kPipe: 64-row, 64-column units
     uint64_t threads;            // of the grid
 };
 
@@ -1279,8 +1271,8 @@ hipError_t launch(I8Args& p, hipStream_t stream) {
         if (f.ns == 2) return launch_staged<O, 2, 4, 4, 2>(p, stream);
         return launch_staged<O, 4, 4, 2, 4>(p, stream);
     }
-    if (f.ns == 1) return launch_split<O, 1, 1, 8>(p, stream);
-    return launch_split<O, 1, 2, 8>(p, stream);
+    if (f.ns == 1) return launch_split<O, 1, 8>(p, stream);
+    return launch_split<O, 2, 8>(p, stream);
 }
 
 }  // namespace
