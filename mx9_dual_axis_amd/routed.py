@@ -136,7 +136,7 @@ def _valid(valid, T, i):
 def _out_matrix(out, name, shape, dtype, like):
     """`out`, or a new matrix on the device of `like`; and its row pitch."""
     if out is None:
-        return like.new_empty(shape, dtype=dtype), shape[1]
+        return like.new_empty_strided(shape, (shape[1], 1), dtype=dtype), shape[1]   # the quickest of torch's ways
     pitch = _matrix(out, name, (dtype,), like.get_device())[0]
     if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(out.shape)}")
@@ -276,8 +276,7 @@ def _codes_out(out, rows, K, like):
     products read fastest."""
     if out is None:
         pitch = (K + 15) // 16 * 16
-        q = like.new_empty((rows, pitch), dtype=_I8)
-        return (q if pitch == K else q[:, :K]), pitch, like.new_empty((rows,), dtype=_F32)
+        return like.new_empty_strided((rows, K), (pitch, 1), dtype=_I8), pitch, like.new_empty_strided((rows,), (1,), dtype=_F32)
     q, s = out
     if q is None:
         raise ValueError("out must be two tensors, the codes and the scales")
@@ -316,7 +315,7 @@ def _product_out(out, shape, out_dtype, like):
     if out is None:
         if out_dtype not in _ESZ:
             raise ValueError(f"out_dtype must be float32 or bfloat16, not {out_dtype}")
-        return like.new_empty(shape, dtype=out_dtype), shape[1]
+        return like.new_empty_strided(shape, (shape[1], 1), dtype=out_dtype), shape[1]
     if out.dtype not in _ESZ:
         raise ValueError(f"out must be float32 or bfloat16, not {out.dtype}")
     return _out_matrix(out, "out", shape, out.dtype, like)
@@ -350,7 +349,7 @@ def i8_linear(x: torch.Tensor, B: torch.Tensor, sB: torch.Tensor, bias: torch.Te
     sb, bi = _flat(sB, "sB", _F32, (N,), i), _bias(bias, N, i)
     out, ldc = _product_out(out, (M, N), out_dtype or x.dtype, x)
     size = M * ((K + 15) // 16 * 16) + (M * 4 + 15) // 16 * 16
-    ws = x.new_empty((size,), dtype=torch.uint8)
+    ws = x.new_empty_strided((size,), (1,), dtype=torch.uint8)
     _run(i, _L().i8_linear, x.data_ptr(), _ESZ[x.dtype], ld, B.data_ptr(), ldb, sb, bi, M, N, K, out.data_ptr(), ldc,
          _ESZ[out.dtype], ws.data_ptr(), size)
     return out
@@ -411,7 +410,7 @@ def mx_combine_grad(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, we
     drows, dweight = out if out is not None else (None, None)
     drows, ld_d = _out_matrix(drows, "out[0]", (M, N), dy.dtype, dy)
     if dweight is None:
-        dweight = dy.new_empty((T, k), dtype=_F32)
+        dweight = dy.new_empty_strided((T, k), (k, 1), dtype=_F32)
     dp = _flat(dweight, "out[1]", _F32, (T, k), i)
     _run(i, _L().mx_combine_grad, dy.data_ptr(), _ESZ[dy.dtype], T, N, ld_g, rows.data_ptr(), ld_r, sp, wp, rp, k, M,
          drows.data_ptr(), ld_d, dp)
