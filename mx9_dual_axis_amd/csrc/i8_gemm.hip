@@ -663,6 +663,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_pipe_kernel(I8Args p) {
 // by ordinary loads (which take any address), wait in registers through the
 // step before theirs, and are written to the slot that the step before that one
 // has left.  Near a row's end the row's last piece is shifted, zeros behind it.
+// The loads' rate bounds it (about a clock a lane where they straddle dwords),
+// not their latency: two or four steps under way in registers instead of one
+// took 19.4 and 19.7 us for 20.1 (128 x 8191 x 4095, 64 x 64 tiles), 46.5 and 48.9
+// for 44.5 (512 rows, 128 x 64; two and three).
 template <typename O, int MS, int NS, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void i8_staged_kernel(I8Args p) {
     using P = Pipe<MS, NS, WM, WN, 2, 2>;
