@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs p) {
 struct QuantArgs {
     const char* x;
     int64_t T, K, ld_x;          // elements, bytes
-    const int32_t *slot, *src;   // null: row t goes to row t
+    const int32_t *slot, *src;   // src null: no map, row t goes to row t
     int32_t k;
     int64_t M;
     int8_t* q;
@@ -206,9 +206,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs p) {
         return;
     }
     const int64_t tok = blockIdx.x;
-    const int32_t n = p.slot ? p.k : 1;
+    const int32_t n = p.src ? p.k : 1;
     if (t < uint32_t(n)) {
-        const int64_t r = p.slot ? int64_t(p.slot[tok * n + t]) : tok;
+        const int64_t r = p.src ? int64_t(p.slot[tok * n + t]) : tok;
         rows[t] = r >= 0 && r < p.M ? int32_t(r) : -1;
     }
     const char* x = p.x + tok * p.ld_x;
@@ -459,7 +459,7 @@ hipError_t launch_quantize_rows(const void* x, int dtype, int64_t T, int64_t K, 
     QuantArgs p;
     p.x = static_cast<const char*>(x); p.T = T; p.K = K; p.ld_x = ld_x * esz; p.slot = slot; p.src = src; p.k = k;
     p.M = M; p.q = q; p.ld_q = ld_q; p.s = s;
-    const dim3 grid(uint32_t(slot ? token_blocks(T, M) : uint64_t(T))), block(kThreads);
+    const dim3 grid(uint32_t(src ? token_blocks(T, M) : uint64_t(T))), block(kThreads);
     if (dtype == 0) hipLaunchKernelGGL(quantize_kernel<float>, grid, block, 0, stream, p);
     else hipLaunchKernelGGL(quantize_kernel<uint16_t>, grid, block, 0, stream, p);
     return hipGetLastError();
