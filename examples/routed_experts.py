@@ -12,6 +12,11 @@ autograd function over the library's forward and backward calls:
     Experts  mx_grouped_gemm_rows          mx_grouped_gemm_rows (rows), mx_grouped_gemm_k (weights)
     Combine  mx_combine          backward  mx_combine_grad
 
+The backward calls read the routing again, which the next mx_route on the same
+buffers writes over: each function notes the routing's generation and its
+backward refuses another one.  Micro-batches, or layers, that are alive at once
+take a routing each.
+
 Serving: the trained weights become int8 codes with a scale per output
 channel, tokens are quantized on their way to the experts (groups padded to
 one row), and the whole step is captured once in a graph and replayed.
@@ -34,24 +39,28 @@ class Route(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, plan, valid):
-        ctx.save_for_backward(logits)
-        ctx.plan, ctx.valid = mxq.mx_route(logits, valid=valid, out=plan), valid
+        ctx.save_for_backward(logits, valid)
+        ctx.plan = mxq.mx_route(logits, valid=valid, out=plan)
+        ctx.generation = plan.generation
         return plan.weight.clone(), plan.loss.clone()     # the plan's own are written again by the next call
 
     @staticmethod
     def backward(ctx, dweight, dloss):
-        (logits,) = ctx.saved_tensors
-        return mxq.mx_route_grad(logits, ctx.plan, dweight.contiguous(), dloss.contiguous(), ctx.valid), None, None
+        logits, valid = ctx.saved_tensors
+        dlogits = mxq.mx_route_grad(logits, ctx.plan, dweight.contiguous(), dloss.contiguous(), valid,
+                                    generation=ctx.generation)
+        return dlogits, None, None
 
 
 class Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
+        ctx.plan, ctx.generation = plan, plan.generation
         return mxq.mx_dispatch(x, plan.slot, plan.src)
 
     @staticmethod
     def backward(ctx, drows):
+        ctx.plan.require(ctx.generation)
         return mxq.mx_combine(drows.contiguous(), ctx.plan.slot), None
 
 
@@ -66,11 +75,12 @@ class Experts(torch.autograd.Function):
         q, s, qt, st = mxq.mx_quantize_grouped(rows, plan.offs)
         w, sw, wt, swt = mxq.mx_quantize_2d_dual(W.reshape(E * N, K))
         ctx.save_for_backward(qt, st, wt, swt)
-        ctx.plan, ctx.shape = plan, (E, N, K)
+        ctx.plan, ctx.generation, ctx.shape = plan, plan.generation, (E, N, K)
         return mxq.mx_grouped_gemm_rows(q, s, w.view(E, N, K), sw.view(E, N, K // 32), plan.offs, torch.bfloat16)
 
     @staticmethod
     def backward(ctx, dy):
+        ctx.plan.require(ctx.generation)
         qt, st, wt, swt = ctx.saved_tensors
         E, N, K = ctx.shape
         offs = ctx.plan.offs
@@ -85,11 +95,12 @@ class Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weight, plan):
         ctx.save_for_backward(rows, weight)
-        ctx.plan = plan
+        ctx.plan, ctx.generation = plan, plan.generation
         return mxq.mx_combine(rows, plan.slot, weight)
 
     @staticmethod
     def backward(ctx, dy):
+        ctx.plan.require(ctx.generation)
         rows, weight = ctx.saved_tensors
         drows, dweight = mxq.mx_combine_grad(dy.contiguous(), rows, ctx.plan.slot, weight, ctx.plan.src)
         return drows, dweight, None
@@ -101,7 +112,8 @@ def gated(a):
 
 
 def train_layer(x, params, plan, valid=None):
-    """x bf16 [T, K] -> (y bf16 [T, K], balance loss)."""
+    """x bf16 [T, K] -> (y bf16 [T, K], balance loss).  `plan` is this pass's
+    until its backward is done."""
     router, W1, W2 = params
     weight, balance = Route.apply(x.float() @ router.t(), plan, valid)
     rows = Dispatch.apply(x, plan)
