@@ -148,15 +148,15 @@ class MXRouting:
     call to call; made by mx_routing.
 
     idx, weight, slot [T, k]; src [rows]; counts, offs, prob [E]; live, loss
-    [1]: see mx_route.  `normalize` is what the last mx_route used and
-    `generation` how many have written here (replays of a captured graph are
-    not counted): what needs the same routing later, a backward pass above all,
-    notes the generation and hands it to mx_route_grad or `require`.  The
-    tensors stay the plan's own: none can be put in another's place, and none
-    may be resized."""
+    [1]: see mx_route.  `normalize` is what the last mx_route used, `masked`
+    whether it was given `valid`, `generation` how many have written here
+    (replays of a captured graph are not counted): what needs the same routing
+    later, a backward pass above all, notes the generation and hands it to
+    mx_route_grad or `require`.  The tensors stay the plan's own: none can be
+    put in another's place, and none may be resized."""
 
-    __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "generation", "idx", "weight", "slot", "src",
-                 "counts", "offs", "live", "prob", "loss", "_workspace", "_ptrs")
+    __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "masked", "generation", "idx", "weight", "slot",
+                 "src", "counts", "offs", "live", "prob", "loss", "_workspace", "_ptrs")
 
     def __setattr__(self, name, value):
         if hasattr(self, "_ptrs") and name != "normalize":
@@ -175,7 +175,7 @@ class MXRouting:
             raise ValueError("device must be a GPU")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.device, self.normalize, self.generation = dev, True, 0
+        self.device, self.normalize, self.masked, self.generation = dev, True, False, 0
         e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
         self.idx, self.weight, self.slot = e((T, k), _I32), e((T, k), _F32), e((T, k), _I32)
         self.src, self.counts, self.offs = e((self.rows,), _I32), e((E,), _I32), e((E,), _I32)
@@ -193,7 +193,8 @@ class MXRouting:
 
 
 # What a call leaves in a routing, past the guard above.
-_set_normalize, _set_generation = MXRouting.normalize.__set__, MXRouting.generation.__set__
+_set_normalize, _set_masked = MXRouting.normalize.__set__, MXRouting.masked.__set__
+_set_generation = MXRouting.generation.__set__
 
 
 def mx_routing(T: int, E: int, k: int, align: int = 128, device="cuda") -> MXRouting:
@@ -228,6 +229,7 @@ def mx_route(logits: torch.Tensor, k: int | None = None, valid: torch.Tensor | N
     _run(i, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), out.k,
          1 if normalize else 0, out.align, out.rows, *out._ptrs)
     _set_normalize(out, bool(normalize))
+    _set_masked(out, valid is not None)
     _set_generation(out, out.generation + 1)
     return out
 
@@ -236,13 +238,17 @@ def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tenso
                   dloss: torch.Tensor | None = None, valid: torch.Tensor | None = None,
                   out: torch.Tensor | None = None, generation: int | None = None) -> torch.Tensor:
     """Gradient of the routing's weight (dweight float32 [T, k]) and loss
-    (dloss float32 [1]) with respect to the logits, in their dtype.  With
-    `generation` (the routing's, noted after its mx_route) a routing that has
-    been written since is refused."""
+    (dloss float32 [1]) with respect to the logits, in their dtype.  The routing
+    does not keep its `valid`: a call without it is refused where mx_route had
+    one, since the tokens it left out would get a gradient.  With `generation`
+    (the routing's, noted after its mx_route) a routing that has been written
+    since is refused."""
     ld, T, E = _matrix(logits, "logits", _ESZ)
     i = logits.get_device()
     if routing.T != T or routing.E != E or routing.device.index != i:
         raise ValueError("routing was made for other logits")
+    if valid is None and routing.masked:
+        raise ValueError("mx_route was given valid, its gradient needs it too")
     if generation is not None:
         routing.require(generation)
     dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), i)

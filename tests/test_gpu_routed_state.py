@@ -117,3 +117,28 @@ def test_gradient_names_the_generation_it_is_of():
     with pytest.raises(ValueError):
         mxq.mx_route(z[:, :5], out=plan)                  # refused: nothing was written
     assert plan.generation == 2
+
+
+# ---- tokens left out
+@pytest.mark.parametrize("filler", [float("nan"), 0.0])
+def test_gradient_without_the_mask_of_its_routing(filler):
+    """Tokens that the routing left out have no gradient: a call that does not
+    say which they are is refused."""
+    T, E, k = 90, 16, 3
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    z = torch.randn((T, E), generator=g, device=DEV)
+    valid = torch.rand(T, generator=g, device=DEV) < 0.7
+    z[~valid] = filler
+    dl = torch.ones(1, device=DEV)
+    r = mxq.mx_route(z, k, valid=valid)
+    d = mxq.mx_route_grad(z, r, dloss=dl, valid=valid)
+    assert not d[~valid].any() and d[valid].any()
+    with pytest.raises(ValueError, match="valid"):
+        mxq.mx_route_grad(z, r, dloss=dl)
+    z[~valid] = 0
+    mxq.mx_route(z, k, out=r)                             # the next routing takes every token
+    assert mxq.mx_route_grad(z, r, dloss=dl).isfinite().all()
+    # a gradient of fewer tokens than were routed: that of the others is 0
+    d = mxq.mx_route_grad(z, r, dloss=dl, valid=valid)
+    assert not d[~valid].any() and torch.equal(d[valid], mxq.mx_route_grad(z, r, dloss=dl)[valid])
