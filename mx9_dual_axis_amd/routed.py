@@ -185,6 +185,14 @@ class MXRouting:
         self._ptrs = tuple(t.data_ptr() for t in (self.idx, self.weight, self.slot, self.src, self.counts, self.offs,
                                                   self.live, self.prob, self.loss, self._workspace)) + (size,)
 
+    def record_stream(self, stream) -> None:
+        """As a tensor's: before the routing is dropped, name every other stream
+        that calls on it were made on, so that its memory (the workspace's too)
+        is not handed out while they work."""
+        for t in (self.idx, self.weight, self.slot, self.src, self.counts, self.offs, self.live, self.prob, self.loss,
+                  self._workspace):
+            t.record_stream(stream)
+
     def require(self, generation: int) -> None:
         """Raise unless this is still the routing of that generation."""
         if generation != self.generation:
@@ -201,9 +209,9 @@ def mx_routing(T: int, E: int, k: int, align: int = 128, device="cuda") -> MXRou
     """The buffers of mx_route for T tokens, E experts and k picks each, groups
     padded to multiples of `align` (128 for the MXFP8 grouped calls).  Each
     mx_route writes them anew: streams that run at once, and forward passes
-    whose backward is still to come, need a routing each, and
-    one that is used on another stream than it was made on is kept until that
-    work is done, as any tensor."""
+    whose backward is still to come, need a routing each.  The calls do not keep
+    its memory: where another stream than the one it was made on works on it,
+    hold the routing until that work is done, or record_stream it."""
     return MXRouting(T, E, k, align, device)
 
 

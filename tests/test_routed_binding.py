@@ -1,0 +1,58 @@
+"""Checks of the routed-expert binding itself."""
+import pytest
+import torch
+
+from helpers import DEV, require_gpu
+from mx9_dual_axis_amd import routed
+
+
+class Memory:
+    """Stands for a tensor: notes the streams that it is said to be used on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_a_routing_used_on_another_stream_holds_all_its_memory():
+    """Nothing of a routing, its workspace included, may go back to the
+    allocator while another stream still works on it."""
+    r = object.__new__(routed.MXRouting)
+    names = ("idx", "weight", "slot", "src", "counts", "offs", "live", "prob", "loss", "_workspace")
+    for n in names:
+        object.__setattr__(r, n, Memory())
+    object.__setattr__(r, "_ptrs", ())
+    stream = object()
+    r.record_stream(stream)
+    assert [getattr(r, n).streams for n in names] == [[stream]] * len(names)
+
+
+@pytest.mark.gpu
+def test_memory_recorded_on_a_stream_is_not_handed_out():
+    """While a stream that a dropped routing was recorded on is at work, new
+    tensors get other memory."""
+    require_gpu()
+    T = 1 << 20                                           # idx, weight and slot: blocks of 8 MiB each
+    plan = routed.mx_routing(T, 4, 2, align=1, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a, z = torch.randn(8192, 8192, device=DEV), torch.randn(T, 4, device=DEV)
+        (a @ a).sum()
+        side.synchronize()
+        b = [a @ a for _ in range(8)]                     # some 10 ms each
+        routed.mx_route(z, out=plan)
+        done = torch.cuda.Event()
+        done.record(side)
+    plan.record_stream(side)
+    held = {t.data_ptr() for t in (plan.idx, plan.weight, plan.slot)}
+    del plan
+    new = [torch.empty((T, 2), dtype=torch.int32, device=DEV) for _ in range(3)]
+    at_work = not done.query()
+    torch.cuda.synchronize()
+    del b
+    if not at_work:
+        pytest.skip("the other stream was done too early to tell")
+    assert held.isdisjoint(t.data_ptr() for t in new)
