@@ -63,8 +63,10 @@ def _L():
     return _lib
 
 
-_device = torch._C._cuda_getDevice
-_stream = torch._C._cuda_getCurrentRawStream
+# The current device's index and a device's current stream: torch's quickest
+# ways, which are private, or its public ones where a torch has no such names.
+_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _run(i, f, *args):

@@ -1,9 +1,15 @@
 """Checks of the routed-expert binding itself."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from helpers import DEV, require_gpu
 from mx9_dual_axis_amd import routed
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Memory:
@@ -56,3 +62,25 @@ def test_memory_recorded_on_a_stream_is_not_handed_out():
     if not at_work:
         pytest.skip("the other stream was done too early to tell")
     assert held.isdisjoint(t.data_ptr() for t in new)
+
+
+def test_the_package_needs_no_private_name_of_torch():
+    """The calls' quick ways to the current device and stream are private to
+    torch: without them (a torch built without a GPU, a later one) the package
+    imports and its public ones are used."""
+    code = """
+import torch
+for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, n):
+        delattr(torch._C, n)
+from mx9_dual_axis_amd import routed
+torch.cuda.current_device = lambda: 3
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_stream = lambda i: Stream if i == 3 else None
+assert routed._device() == 3 and routed._stream(3) == 77
+seen = []
+routed._run(3, lambda *a: seen.append(a), 5)
+assert seen == [(5, 77)]
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
