@@ -73,7 +73,7 @@ int64_t mx_route_workspace(int64_t T, int32_t E);
  * mx_route_rows or above 2^30, workspace_bytes too small), MX_E_STRIDE
  * (ld < E), MX_E_ALIGN (a pointer not aligned to its element),
  * MX_E_OVERLAP.  T == 0 writes empty groups.  Up to 64 tokens one kernel,
- * otherwise three.
+ * otherwise two, or three where the blocks' counts are much to add.
  */
 int mx_route(const void *logits, int32_t dtype, int64_t T, int32_t E, int64_t ld, const uint8_t *valid,
              int32_t k, int32_t normalize, int32_t align, int64_t M, int32_t *idx, float *weight, int32_t *slot,
@@ -110,7 +110,8 @@ int mx_route_grad(const void *logits, int32_t dtype, int64_t T, int32_t E, int64
  * Errors: MX_E_NULL, MX_E_DTYPE, MX_E_SHAPE (a negative size, T k or M above
  * 2^30, rows above 2^30 elements, k outside [1, 64], a grid above 2^32
  * threads), MX_E_STRIDE (a pitch below its row, a span above 2^48 bytes),
- * MX_E_ALIGN, MX_E_OVERLAP.  N == 0 (K == 0 for mx_dispatch) is a no-op.
+ * MX_E_ALIGN, MX_E_OVERLAP.  Rows of no elements: mx_dispatch is a no-op,
+ * the quantizing calls still write s (2^-126).
  */
 int mx_dispatch(const void *x, int32_t dtype, int64_t T, int64_t N, int64_t ld_x, const int32_t *slot,
                 const int32_t *src, int32_t k, int64_t M, void *out, int64_t ld_out, void *stream);
@@ -163,7 +164,8 @@ int i8_grouped_gemm_rows(const int8_t *A, int64_t lda, const float *sA, const in
  * src[r] < 0 are 0; dweight[t][j] = <dy[t], rows[slot[t][j]]> in fp32, 0 for a
  * pick without a slot.  dweight NULL: not computed (rows may be NULL then).
  *
- * Errors as for mx_dispatch.
+ * Errors as for mx_dispatch.  N == 0: mx_combine is a no-op, mx_combine_grad
+ * still writes dweight (0).
  */
 int mx_combine(const void *rows, int32_t dtype, int64_t M, int64_t N, int64_t ld_r, const int32_t *slot,
                const float *weight, int32_t k, int64_t T, void *y, int64_t ld_y, void *stream);

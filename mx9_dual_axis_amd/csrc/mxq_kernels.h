@@ -86,10 +86,12 @@ hipError_t launch_route_grad(const void* logits, int dtype, int64_t T, int32_t E
                              int64_t ld_d, hipStream_t stream);
 
 // Token rows to and from their experts' rows (routed_rows.hip); pitches in
-// elements, N, K > 0.  launch_quantize_rows with src == nullptr sends row t
-// to row t (M = T > 0); with a map M > 0, and T may be 0 (slot null then).
-// combine and combine_grad: weight null means 1; dweight may be null.  The
-// *_blocks functions give the grids.
+// elements.  launch_dispatch and launch_combine need N > 0; the others take
+// rows of no elements too, and write their scales or dweight.
+// launch_quantize_rows with src == nullptr sends row t to row t (M = T > 0);
+// with a map M > 0, and T may be 0 (slot null then).  combine and
+// combine_grad: weight null means 1; dweight may be null.  The *_blocks
+// functions give the grids.
 uint64_t dispatch_blocks(int64_t T, int64_t M, int64_t row_bytes);
 uint64_t combine_blocks(int64_t T, int64_t row_bytes);
 uint64_t token_blocks(int64_t T, int64_t M);
