@@ -68,11 +68,17 @@ const Tile& best_tile(const Tile (&tiles)[kN], int64_t M, int64_t N, int64_t K, 
 //   rows  32: 135.1  116.8  131.9  rows 256:        262.9  236.8
 //   rows  64:        152.9  137.6  rows 512:        482.1  411.4
 // (64 rows to each expert alike: 120.8 and 136.0; the 671 MB of weights alone
-// take 108 us at 6.2 TB/s).
+// take 108 us at 6.2 TB/s).  The thresholds come from that one shape; few rows
+// of few experts make too few tiles of 256 columns (1, 2, 4 and 8 tokens with 4
+// picks of these experts: 33, 35, 38 and 47 us, the picked experts' weights
+// alone 7, 14, 26 and 46).
 //
 // Dense in whole pieces: with the times below the choice is the fastest of the
 // five tiles at each of the 42 shapes where all were timed (M 32 to 8192; N, K
-// 14336 x 4096, 8192 x 8192 and 2048 x 5120).
+// 14336 x 4096, 8192 x 8192 and 2048 x 5120).  No tile splits the contraction:
+// past the ring's 16 rows each workgroup walks all of it, however few there are
+// (16, 17 and 64 rows: [8192, 8192] 14.2, 23.3 and 24.1 us; [1024, 8192] 7.6, 21.4
+// and 21.7).
 //
 // Rows at any byte, dense [8191, 4095] and the same (us for tiles of 64 x 64, 128
 // x 64, 128 x 128, 128 x 256; the last form is 16 x 16 split):

@@ -24,7 +24,7 @@
 //          streams its share through LDS for itself.  One token through [14336,
 //          4096]: 12.1 us, its quantization within, 58.7 MB at 4.9 TB/s.
 //   pipe   operands in whole 16-byte pieces: tiles of 64 x 64 to 256 x 256,
-//          loads straight to LDS.  8192 cubed: 430 to 490 us (2.2 to 2.6 PFLOP/s;
+//          loads straight to LDS.  8192 cubed: 430 to 525 us (2.1 to 2.6 PFLOP/s;
 //          the clock falls as the matrix cores fill), 64 experts of [2048, 5120]
 //          with 2 rows each 87 us (the weights' 580 MB), with 256 245 us.
 //   split  rows that start at any byte, few tiles: the waves of a workgroup

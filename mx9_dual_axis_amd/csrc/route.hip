@@ -720,9 +720,9 @@ constexpr int kGradThr = 256;
 // latency of a row's loads.  A row's memory is therefore read a round ahead
 // (up to 256 experts, where the registers allow four waves a SIMD), and the
 // loss's part of each expert stays in LDS, not in registers.  131072 tokens of
-// 256 fp32 scores take 51 us (their bytes alone, as a copy's, 54; 58 without
-// either measure), of 256 bf16 scores 42 (27; 59), 65536 of 384 bf16 scores 40
-// (20; 90).
+// 256 fp32 scores take 51 us (a copy kernel moves as many bytes in 54; 58
+// without either measure), of 256 bf16 scores 42 (27; 59), 65536 of 384 bf16
+// scores 40 (20; 90).
 template <typename L, int V>
 __global__ __launch_bounds__(kGradThr) void route_grad_kernel(RouteGradArgs p) {
     using S = Scores<L, V>;
