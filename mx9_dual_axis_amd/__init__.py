@@ -24,8 +24,9 @@ when ``offs`` is None, grouped otherwise), ``convert_to_mx9`` and
 
 ``routed`` holds what stands between the tokens of a routed-expert layer and
 these calls (routing with its balance loss, dispatch, combine, their
-gradients) and the product of 8-bit integer codes; its names are the package's
-too.
+gradients) and the product of 8-bit integer codes; ``act`` the products of both
+kinds with bias, activation and residual in their epilogue.  Their names are
+the package's too.
 """
 from __future__ import annotations
 
@@ -694,3 +695,5 @@ def convert_from_mx9_packed(packed, out_dtype, shape, block_size: int = 16, axis
 
 from .routed import (MXRouting, i8_gemm_nt, i8_grouped_gemm_rows, i8_linear, i8_quantize_rows,  # noqa: E402,F401
                      mx_combine, mx_combine_grad, mx_dispatch, mx_dispatch_i8, mx_route, mx_route_grad, mx_routing)
+from .act import (i8_gemm_nt_act, i8_grouped_gemm_rows_act, i8_linear_act, mx_act_grad, mx_gemm_nt_act,  # noqa: E402,F401
+                  mx_gemm_nt_act_mfma, mx_grouped_gemm_rows_act, mx_grouped_gemm_rows_act_mfma)

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmxq.so")
 ROOF_LIB = os.path.join(HERE, "libmxq_roof.so")
 SOURCES = ["dual_axis.hip", "mx9.hip", "mx9_layouts.hip", "mx_gemm.hip", "scale_layout.hip", "mxq_abi.cpp",
-           "route.hip", "routed_rows.hip", "i8_gemm.hip", "routed_abi.cpp"]
+           "route.hip", "routed_rows.hip", "i8_gemm.hip", "routed_abi.cpp",
+           "i8_act.hip", "i8_act_gated.hip", "mx_act.hip", "mx_act_gated.hip", "act_grad.hip", "act_abi.cpp"]
 ROOF_SOURCES = ["roof.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -38,7 +39,7 @@ def _link(sources, out, objdir, verbose):
         lang = ["-x", "hip"] if src.endswith(".cpp") else []
         cmds.append([HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
-    with ThreadPoolExecutor(max_workers=min(6, len(cmds))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
     tmp = out + ".tmp"

@@ -90,52 +90,6 @@ int check_mx9_view(int32_t dtype, int64_t outer, int64_t len, int64_t inner, int
     return MX_OK;
 }
 
-// Bytes spanned by a strided scale view of rows x blocks (non-negative strides).
-uint64_t scale_span(int64_t rows, int64_t blocks, int64_t rs, int64_t bs) {
-    if (rows <= 0 || blocks <= 0) return 0;
-    return uint64_t((rows - 1) * rs + (blocks - 1) * bs + 1);
-}
-
-constexpr int64_t kMaxGemm = int64_t(1) << 24;
-
-// Checks shared by the contraction calls: operand pitches and alignment,
-// scale strides, the output type and pitch.  K is the contraction extent.
-int check_gemm(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int64_t sa_bs,
-               const uint8_t* B, int64_t ldb, const uint8_t* sB, int64_t sb_rs, int64_t sb_bs,
-               int64_t M, int64_t N, int64_t K, const void* C, int64_t ldc, int32_t out_dtype, bool mfma) {
-    const bool empty = M == 0 || N == 0;
-    if (!empty && (!A || !sA || !B || !sB || !C)) return MX_E_NULL;
-    if (out_dtype != MX_DTYPE_F32 && out_dtype != MX_DTYPE_BF16) return MX_E_DTYPE;
-    if (M < 0 || N < 0 || K < 0 || M > kMaxGemm || N > kMaxGemm || K > kMaxGemm ||
-        M % 128 != 0 || N % 128 != 0 || K % 128 != 0)
-        return MX_E_SHAPE;
-    if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0 || lda > kMaxGemm || ldb > kMaxGemm || ldc < N ||
-        ldc > kMaxGemm || sa_rs < 0 || sa_bs < 0 || sb_rs < 0 || sb_bs < 0)
-        return MX_E_STRIDE;
-    const uintptr_t esz = out_dtype == MX_DTYPE_F32 ? 4 : 2;
-    if (!empty && (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, esz))) return MX_E_ALIGN;
-    if (!empty && mfma && (!aligned(sA, 16) || !aligned(sB, 16))) return MX_E_ALIGN;
-    return MX_OK;
-}
-
-// Whether every contraction kernel the call may launch has a grid whose
-// thread count fits 32 bits: the general kernel (128 x 128 tiles of 256
-// threads), the pipelined kernel (256 x 256 tiles of 512 threads, or for row
-// groups 8 XCD shares of at most ceil(M/128/8) + 1 row tiles of 128 x 256),
-// times the group count for contraction groups.
-bool gemm_grid_fits(int64_t M, int64_t N, int32_t G, bool row_groups, bool k_groups) {
-    const uint64_t g = k_groups ? uint64_t(G) : 1u;
-    const uint64_t general = uint64_t(M / 128) * uint64_t(N / 128) * g * 256u;
-    const uint64_t pipe = row_groups ? 8u * (uint64_t(M / 128 + 7) / 8u + 1u) * uint64_t((N + 255) / 256) * 512u
-                                     : uint64_t((M + 255) / 256) * uint64_t((N + 255) / 256) * g * 512u;
-    return general <= kMaxThreads && pipe <= kMaxThreads;
-}
-
-// Bytes of one operand's scales: a strided view, or rows * K/32 in the matrix-core layout.
-uint64_t scale_bytes(bool mfma, int64_t rows, int64_t K, int64_t rs, int64_t bs) {
-    return mfma ? uint64_t(rows) * uint64_t(K / 32) : scale_span(rows, K / 32, rs, bs);
-}
-
 int gemm_call(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int64_t sa_bs,
               const uint8_t* B, int64_t ldb, const uint8_t* sB, int64_t sb_rs, int64_t sb_bs,
               int64_t M, int64_t N, int64_t K, void* C, int64_t ldc, int32_t out_dtype, bool mfma, void* stream) {
@@ -234,7 +188,7 @@ const char* mx_status_string(int status) {
         case MX_E_NULL: return "MX_E_NULL: a required pointer is NULL";
         case MX_E_DTYPE: return "MX_E_DTYPE: unsupported element type (fp32 or bf16 only)";
         case MX_E_BLOCK: return "MX_E_BLOCK: unsupported block size (32 for MXFP8, 16 for MX9)";
-        case MX_E_MODE: return "MX_E_MODE: unsupported scaling mode (RCEIL only)";
+        case MX_E_MODE: return "MX_E_MODE: unsupported scaling mode (RCEIL only), activation or score";
         case MX_E_SHAPE: return "MX_E_SHAPE: unsupported shape (MXFP8 needs M, N multiples of 128)";
         case MX_E_STRIDE: return "MX_E_STRIDE: row pitch smaller than the row or misaligned";
         case MX_E_ALIGN: return "MX_E_ALIGN: pointer misaligned";

@@ -106,17 +106,64 @@ hipError_t launch_combine_grad(const void* dy, int dtype, int64_t T, int64_t N, 
                                int64_t ld_r, const int32_t* slot, const float* weight, const int32_t* src, int32_t k,
                                int64_t M, void* drows, int64_t ld_d, float* dweight, hipStream_t stream);
 
+// What a product with an epilogue (epilogue.h) does with its sums: bias,
+// activation, residual.
+struct Epilogue {
+    int32_t act;
+    const float* bias;           // null: none
+    int64_t bias_gs;             // of one expert to the next
+    int64_t up;                  // gated: channels from a gate to what it multiplies
+    const void* residual;        // null: none; may be C itself
+    int64_t ld_res;
+    void* pre;                   // null: x is not kept
+    int64_t ld_pre;
+};
+
 // Product of 8-bit codes, C = A B^T with row scales (i8_gemm.hip); offs null:
 // dense.  M, N > 0, K <= 131071.
 uint64_t i8_gemm_threads(int64_t lda, int64_t ldb, int64_t M, int64_t N, int64_t K, bool groups, int32_t G);
 hipError_t launch_i8_gemm(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
                           const float* sB, int64_t sb_gs, const float* bias, void* C, int64_t ldc, int64_t M,
                           int64_t N, int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);
+// The same with an epilogue (i8_act.hip, i8_act_gated.hip), N counting results:
+// gated, B has 2 N rows and e.up = N.
+hipError_t launch_i8_gemm_act(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
+                              const float* sB, int64_t sb_gs, const Epilogue& e, void* C, int64_t ldc, int64_t M, int64_t N,
+                              int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);
+hipError_t launch_i8_gemm_act_gated(const int8_t* A, int64_t lda, const float* sA, const int8_t* B, int64_t ldb, int64_t b_gs,
+                                    const float* sB, int64_t sb_gs, const Epilogue& e, void* C, int64_t ldc, int64_t M,
+                                    int64_t N, int64_t K, const int32_t* offs, int32_t G, int out_dtype, hipStream_t stream);
 // The product of activations that are quantized by the product's own kernel,
 // where i8_linear_fuses says so (few rows of whole 16-code pieces, or few tiles).
 bool i8_linear_fuses(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K);
 hipError_t launch_i8_linear_fused(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, const float* sB,
                                   const float* bias, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
                                   int out_dtype, hipStream_t stream);
+hipError_t launch_i8_linear_fused_act(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb, const float* sB,
+                                      const Epilogue& e, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, int out_dtype,
+                                      hipStream_t stream);
+hipError_t launch_i8_linear_fused_act_gated(const void* x, int dtype, int64_t ld_x, const int8_t* B, int64_t ldb,
+                                            const float* sB, const Epilogue& e, void* C, int64_t ldc, int64_t M, int64_t N,
+                                            int64_t K, int out_dtype, hipStream_t stream);
+
+// The MXFP8 contraction with an epilogue, dense or by row groups (mx_act.hip,
+// mx_act_gated.hip); N counts results, a multiple of 128.
+hipError_t launch_mx_act(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int64_t sa_bs, const uint8_t* B,
+                         int64_t ldb, int64_t b_gs, const uint8_t* sB, int64_t sb_rs, int64_t sb_bs, int64_t sb_gs,
+                         const Epilogue& e, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K, const int32_t* offs,
+                         int32_t G, int out_dtype, bool mfma_scales, hipStream_t stream);
+hipError_t launch_mx_act_gated(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int64_t sa_bs,
+                               const uint8_t* B, int64_t ldb, int64_t b_gs, const uint8_t* sB, int64_t sb_rs, int64_t sb_bs,
+                               int64_t sb_gs, const Epilogue& e, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                               const int32_t* offs, int32_t G, int out_dtype, bool mfma_scales, hipStream_t stream);
+
+// Gradient of an epilogue (act_grad.hip): dpre, and with dbias its sums by
+// channel over each group's rows (offs null: all rows).  N > 0; M = 0 still
+// writes dbias.  workspace: act_grad_workspace bytes where dbias is wanted.
+int64_t act_grad_workspace(int64_t M, int64_t N, int dtype, bool gated, bool groups, int32_t G);
+uint64_t act_grad_threads(int64_t M, int64_t N, int dtype, bool groups, int32_t G);   // of one of the grid's rows
+hipError_t launch_act_grad(const void* dy, int64_t ld_dy, const void* pre, int64_t ld_pre, int dtype, int64_t M, int64_t N,
+                           int act, bool gated, const int32_t* offs, int32_t G, void* dpre, int64_t ld_d, float* dbias,
+                           float* workspace, hipStream_t stream);
 
 }  // namespace mxq

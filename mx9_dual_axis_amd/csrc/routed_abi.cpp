@@ -13,24 +13,6 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int64_t kMaxCodes = 131071;     // 131071 * 128 * 128 < 2^31
-
-hipStream_t hip(void* stream) { return static_cast<hipStream_t>(stream); }
-int status(hipError_t e) { return e == hipSuccess ? MX_OK : MX_E_LAUNCH; }
-
-bool dtype_ok(int32_t d) { return d == MX_DTYPE_F32 || d == MX_DTYPE_BF16; }
-int64_t elem(int32_t d) { return d == MX_DTYPE_F32 ? 4 : 2; }
-
-// The first n_out spans are outputs: disjoint from each other and from the
-// inputs that follow; inputs may overlap each other.
-bool outputs_clash(const Span* s, int n_out, int n) {
-    for (int i = 0; i < n_out; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if (overlap(s[i], s[j])) return true;
-    return false;
-}
-
 bool route_shape(int64_t T, int32_t E, int32_t k) {
     return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= 16 && k <= E && T <= kMaxRows / k;
 }
