@@ -694,6 +694,7 @@ def convert_from_mx9_packed(packed, out_dtype, shape, block_size: int = 16, axis
 
 
 from .routed import (MXRouting, i8_gemm_nt, i8_grouped_gemm_rows, i8_linear, i8_quantize_rows,  # noqa: E402,F401
-                     mx_combine, mx_combine_grad, mx_dispatch, mx_dispatch_i8, mx_route, mx_route_grad, mx_routing)
+                     mx_combine, mx_combine_grad, mx_dispatch, mx_dispatch_i8, mx_route, mx_route_bias_step,
+                     mx_route_grad, mx_route_scored, mx_route_scored_grad, mx_routing)
 from .act import (i8_gemm_nt_act, i8_grouped_gemm_rows_act, i8_linear_act, mx_act_grad, mx_gemm_nt_act,  # noqa: E402,F401
                   mx_gemm_nt_act_mfma, mx_grouped_gemm_rows_act, mx_grouped_gemm_rows_act_mfma)

@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libmxq.so")
 ROOF_LIB = os.path.join(HERE, "libmxq_roof.so")
 SOURCES = ["dual_axis.hip", "mx9.hip", "mx9_layouts.hip", "mx_gemm.hip", "scale_layout.hip", "mxq_abi.cpp",
            "route.hip", "routed_rows.hip", "i8_gemm.hip", "routed_abi.cpp",
-           "i8_act.hip", "i8_act_gated.hip", "mx_act.hip", "mx_act_gated.hip", "act_grad.hip", "act_abi.cpp"]
+           "i8_act.hip", "i8_act_gated.hip", "mx_act.hip", "mx_act_gated.hip", "act_grad.hip", "act_abi.cpp",
+           "route_scored.hip", "scored_abi.cpp"]
 ROOF_SOURCES = ["roof.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

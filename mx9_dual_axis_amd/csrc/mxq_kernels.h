@@ -85,6 +85,20 @@ hipError_t launch_route_grad(const void* logits, int dtype, int64_t T, int32_t E
                              const int32_t* counts, const int32_t* live, const float* dloss, void* dlogits,
                              int64_t ld_d, hipStream_t stream);
 
+// Routing by scores (route_scored.hip): groups <= 32 divides E, 1 <= top <=
+// groups, best 1 or 2, k <= top E / groups; the rest as above.
+hipError_t launch_route_scored(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld, const uint8_t* valid,
+                               const float* bias, bool softmax, int32_t groups, int32_t top, int32_t best, int32_t k,
+                               bool normalize, float scale, int32_t align, int64_t M, int32_t* idx, float* weight,
+                               int32_t* slot, int32_t* src, int32_t* counts, int32_t* offs, int32_t* live, float* prob,
+                               float* loss, void* workspace, hipStream_t stream);
+hipError_t launch_route_scored_grad(const void* logits, int dtype, int64_t T, int32_t E, int64_t ld, const uint8_t* valid,
+                                    bool softmax, int32_t k, bool normalize, float scale, const int32_t* idx,
+                                    const float* dweight, const int32_t* counts, const int32_t* live, const float* dloss,
+                                    void* dlogits, int64_t ld_d, hipStream_t stream);
+hipError_t launch_route_bias_step(const float* bias, const int32_t* counts, int32_t E, float rate, float* out,
+                                  hipStream_t stream);
+
 // Token rows to and from their experts' rows (routed_rows.hip); pitches in
 // elements.  launch_dispatch and launch_combine need N > 0; the others take
 // rows of no elements too, and write their scales or dweight.

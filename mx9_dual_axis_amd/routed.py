@@ -1,9 +1,12 @@
-"""Binding of ``include/mxq_routed.h``: routing, dispatch, 8-bit integer
-products and combine of a routed-expert layer.
+"""Binding of ``include/mxq_routed.h`` and ``include/mxq_scored.h``: routing,
+dispatch, 8-bit integer products and combine of a routed-expert layer.
 
   mx_routing(T, E, k, align)              -> an MXRouting, the outputs and workspace of mx_route
   mx_route(logits, k, valid)              -> MXRouting (idx, weight, slot, src, counts, offs, live, prob, loss)
   mx_route_grad(logits, routing, dweight, dloss, valid) -> dlogits
+  mx_route_scored(logits, k, bias, ...)   -> MXRouting, by sigmoid or softmax scores with a bias and groups
+  mx_route_scored_grad(logits, routing, dweight, dloss, valid) -> dlogits
+  mx_route_bias_step(bias, counts, rate)  -> the next bias
   mx_dispatch(x, slot, src)               -> rows of the padded buffer
   mx_dispatch_i8(x, slot, src)            -> (q, s), the same rows as int8 codes and scales
   i8_quantize_rows(x)                     -> (q, s)
@@ -44,6 +47,13 @@ def _argtypes(lib):
     lib.i8_grouped_gemm_rows.argtypes = [P, I64, P, P, I64, I64, P, I64, P, I32, I64, I64, I64, P, I64, I32, P]
     lib.mx_combine.argtypes = [P, I32, I64, I64, I64, P, P, I32, I64, P, I64, P]
     lib.mx_combine_grad.argtypes = [P, I32, I64, I64, I64, P, I64, P, P, P, I32, I64, P, I64, P, P]
+    F = ctypes.c_float
+    lib.mx_route_scored.argtypes = [P, I32, I64, I32, I64, P, P, I32, I32, I32, I32, I32, I32, F, I32, I64, P, P, P, P, P,
+                                    P, P, P, P, P, I64, P]
+    lib.mx_route_scored_grad.argtypes = [P, I32, I64, I32, I64, P, I32, I32, I32, F, P, P, P, P, P, P, I64, P]
+    lib.mx_route_bias_step.argtypes = [P, P, I32, F, P, P]
+    for f in (lib.mx_route_scored, lib.mx_route_scored_grad, lib.mx_route_bias_step):
+        f.restype = ctypes.c_int
     for f in (lib.mx_route, lib.mx_route_grad, lib.mx_dispatch, lib.mx_dispatch_i8, lib.i8_quantize_rows,
               lib.i8_gemm_nt, lib.i8_linear, lib.i8_grouped_gemm_rows, lib.mx_combine, lib.mx_combine_grad):
         f.restype = ctypes.c_int
@@ -146,18 +156,19 @@ def _out_matrix(out, name, shape, dtype, like):
 
 
 class MXRouting:
-    """Outputs and workspace of mx_route for one (T, E, k, align), reused from
-    call to call; made by mx_routing.
+    """Outputs and workspace of mx_route and mx_route_scored for one (T, E, k,
+    align), reused from call to call; made by mx_routing.
 
     idx, weight, slot [T, k]; src [rows]; counts, offs, prob [E]; live, loss
-    [1]: see mx_route.  `normalize` is what the last mx_route used, `masked`
-    whether it was given `valid`, `generation` how many have written here
+    [1]: see mx_route.  `normalize` is what the last call used, `scored` its
+    (score, scale) or None where it was mx_route, `masked` whether it was given
+    `valid`, `generation` how many have written here
     (replays of a captured graph are not counted): what needs the same routing
     later, a backward pass above all, notes the generation and hands it to
     mx_route_grad or `require`.  The tensors stay the plan's own: none can be
     put in another's place, and none may be resized."""
 
-    __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "masked", "generation", "idx", "weight", "slot",
+    __slots__ = ("T", "E", "k", "align", "rows", "device", "normalize", "masked", "generation", "scored", "idx", "weight", "slot",
                  "src", "counts", "offs", "live", "prob", "loss", "_workspace", "_ptrs")
 
     def __setattr__(self, name, value):
@@ -177,7 +188,7 @@ class MXRouting:
             raise ValueError("device must be a GPU")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.device, self.normalize, self.masked, self.generation = dev, True, False, 0
+        self.device, self.normalize, self.masked, self.generation, self.scored = dev, True, False, 0, None
         e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
         self.idx, self.weight, self.slot = e((T, k), _I32), e((T, k), _F32), e((T, k), _I32)
         self.src, self.counts, self.offs = e((self.rows,), _I32), e((E,), _I32), e((E,), _I32)
@@ -204,7 +215,15 @@ class MXRouting:
 
 # What a call leaves in a routing, past the guard above.
 _set_normalize, _set_masked = MXRouting.normalize.__set__, MXRouting.masked.__set__
-_set_generation = MXRouting.generation.__set__
+_set_generation, _set_scored = MXRouting.generation.__set__, MXRouting.scored.__set__
+
+
+def _written(out, normalize, valid, scored):
+    _set_normalize(out, bool(normalize))
+    _set_masked(out, valid is not None)
+    _set_scored(out, scored)
+    _set_generation(out, out.generation + 1)
+    return out
 
 
 def mx_routing(T: int, E: int, k: int, align: int = 128, device="cuda") -> MXRouting:
@@ -229,19 +248,102 @@ def mx_route(logits: torch.Tensor, k: int | None = None, valid: torch.Tensor | N
     MXRouting) k and align are those it was made for."""
     ld, T, E = _matrix(logits, "logits", _ESZ)
     i = logits.get_device()
+    out = _plan(out, logits, T, E, k, align)
+    _run(i, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), out.k,
+         1 if normalize else 0, out.align, out.rows, *out._ptrs)
+    return _written(out, normalize, valid, None)
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def mx_route_scored(logits: torch.Tensor, k: int | None = None, bias: torch.Tensor | None = None, score: str = "sigmoid",
+                    groups: int = 1, top_groups: int | None = None, group_best: int = 2, normalize: bool = True,
+                    scale: float = 1.0, valid: torch.Tensor | None = None, align: int = 128,
+                    out: MXRouting | None = None) -> MXRouting:
+    """Routing of logits [T, E] (float32 or bfloat16, rows at any pitch) by
+    sigmoid or softmax scores s.
+
+    The k experts of largest s + bias (float32 [E]; it decides picks alone) are
+    taken out of the top_groups (None: all) of `groups` groups of neighbouring
+    experts, those whose group_best (1 or 2) largest s + bias sum to most.  The
+    result's weight are scale s of the picks, over their sum when `normalize`.
+    valid, align, out and the rest of the result as for mx_route."""
+    code = SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, not {score!r}")
+    ld, T, E = _matrix(logits, "logits", _ESZ)
+    i = logits.get_device()
+    if top_groups is None:
+        top_groups = groups
+    if not 1 <= groups <= 32 or E % groups or not 1 <= top_groups <= groups or group_best not in (1, 2):
+        raise ValueError(f"{groups} groups (top {top_groups}, best {group_best}) of E={E} experts: 1 to 32 groups of equal "
+                         "size, 1 <= top_groups <= groups, group_best 1 or 2 are needed")
+    b = None if bias is None else _flat(bias, "bias", _F32, (E,), i)
+    v = _valid(valid, T, i)
+    picks = out.k if out is not None else k
+    if picks is not None and picks > top_groups * (E // groups):
+        raise ValueError(f"k={picks} picks out of {top_groups} groups of {E // groups} experts")
+    out = _plan(out, logits, T, E, k, align)
+    _run(i, _L().mx_route_scored, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, v, b, code, groups, top_groups,
+         group_best, out.k, 1 if normalize else 0, scale, out.align, out.rows, *out._ptrs)
+    return _written(out, normalize, valid, (score, float(scale)))
+
+
+def mx_route_scored_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tensor | None = None,
+                         dloss: torch.Tensor | None = None, valid: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, generation: int | None = None) -> torch.Tensor:
+    """mx_route_grad of a routing that mx_route_scored wrote (its score, scale
+    and normalize are the routing's)."""
+    ld, T, E = _matrix(logits, "logits", _ESZ)
+    i = logits.get_device()
+    if routing.scored is None:
+        raise ValueError("the routing was not written by mx_route_scored")
+    dw, dl, v = _grad_inputs(routing, T, E, i, dweight, dloss, valid, generation)
+    out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, logits)
+    p = routing._ptrs
+    score, scale = routing.scored
+    _run(i, _L().mx_route_scored_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, v, SCORES[score], routing.k,
+         1 if routing.normalize else 0, scale, p[0], dw, p[4], p[6], dl, out.data_ptr(), ld_d)
+    return out
+
+
+def mx_route_bias_step(bias: torch.Tensor, counts: torch.Tensor, rate: float, out: torch.Tensor | None = None):
+    """bias + rate sign(mean of counts - counts): float32 [E] for counts int32
+    [E] of a routing (or their sums over ranks); out may be bias itself."""
+    if not isinstance(bias, torch.Tensor) or not bias.is_cuda or bias.dim() != 1:
+        raise ValueError("bias must be a float32 [E] device tensor")
+    i, E = bias.get_device(), bias.shape[0]
+    b, c = _flat(bias, "bias", _F32, (E,), i), _flat(counts, "counts", _I32, (E,), i)
+    if out is None:
+        out = bias.new_empty_strided((E,), (1,))
+    _run(i, _L().mx_route_bias_step, b, c, E, rate, _flat(out, "out", _F32, (E,), i))
+    return out
+
+
+def _plan(out, logits, T, E, k, align):
+    """`out`, checked against the call, or a new routing."""
     if out is None:
         if k is None:
             raise ValueError("k is needed when out is not given")
-        out = MXRouting(T, E, k, align, logits.device)
-    elif out.T != T or out.E != E or out.device.index != i or (k is not None and k != out.k):
+        return MXRouting(T, E, k, align, logits.device)
+    if out.T != T or out.E != E or out.device.index != logits.get_device() or (k is not None and k != out.k):
         raise ValueError(f"out was made for T={out.T}, E={out.E}, k={out.k} on {out.device}, the call has T={T}, "
                          f"E={E}, k={k} on {logits.device}")
-    _run(i, _L().mx_route, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), out.k,
-         1 if normalize else 0, out.align, out.rows, *out._ptrs)
-    _set_normalize(out, bool(normalize))
-    _set_masked(out, valid is not None)
-    _set_generation(out, out.generation + 1)
     return out
+
+
+def _grad_inputs(routing, T, E, i, dweight, dloss, valid, generation):
+    """Pointers of a routing gradient's inputs, checked against the routing."""
+    if routing.T != T or routing.E != E or routing.device.index != i:
+        raise ValueError("routing was made for other logits")
+    if valid is None and routing.masked:
+        raise ValueError("the routing was given valid, its gradient needs it too")
+    if generation is not None:
+        routing.require(generation)
+    dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), i)
+    dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), i)
+    return dw, dl, _valid(valid, T, i)
 
 
 def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tensor | None = None,
@@ -255,17 +357,12 @@ def mx_route_grad(logits: torch.Tensor, routing: MXRouting, dweight: torch.Tenso
     since is refused."""
     ld, T, E = _matrix(logits, "logits", _ESZ)
     i = logits.get_device()
-    if routing.T != T or routing.E != E or routing.device.index != i:
-        raise ValueError("routing was made for other logits")
-    if valid is None and routing.masked:
-        raise ValueError("mx_route was given valid, its gradient needs it too")
-    if generation is not None:
-        routing.require(generation)
-    dw = None if dweight is None else _flat(dweight, "dweight", _F32, (T, routing.k), i)
-    dl = None if dloss is None else _flat(dloss, "dloss", _F32, (1,), i)
+    if routing.scored is not None:
+        raise ValueError("the routing was written by mx_route_scored: its gradient is mx_route_scored_grad")
+    dw, dl, v = _grad_inputs(routing, T, E, i, dweight, dloss, valid, generation)
     out, ld_d = _out_matrix(out, "out", (T, E), logits.dtype, logits)
     p = routing._ptrs
-    _run(i, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, _valid(valid, T, i), routing.k,
+    _run(i, _L().mx_route_grad, logits.data_ptr(), _ESZ[logits.dtype], T, E, ld, v, routing.k,
          1 if routing.normalize else 0, p[0], p[1], dw, p[4], p[6], dl, out.data_ptr(), ld_d)
     return out
 
