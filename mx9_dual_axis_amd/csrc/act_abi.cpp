@@ -108,7 +108,7 @@ int mx_call(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int
                         ldc < N ? -1 : ldc + (W - N), out_dtype, mfma);
     if (rc != MX_OK) return rc;
     if (groups && (G < 1 || G > (1 << 20))) return MX_E_SHAPE;
-    if (!gemm_grid_fits(M, W, G, groups, false)) return MX_E_SHAPE;
+    if (!gemm_grid_fits(M, W, G, groups, false)) return MX_E_SHAPE;     // (smaller tiles are taken where they are few)
     if (groups && !offs) return MX_E_NULL;
     if (!aligned(offs, 4)) return MX_E_ALIGN;
     if (b_gs < 0 || sb_gs < 0) return MX_E_STRIDE;

@@ -909,6 +909,163 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few tiles (products with an epilogue): waves that split the contraction.
+//
+// One workgroup of kSplit waves computes 64 x 64 of B's rows (64 x 32 results
+// where gated).  Wave w takes the steps w, w + kSplit, ... for the whole tile:
+// its operands and scales go straight into a ring of its own in LDS, it waits
+// for nothing but them, and there is no barrier before the waves' sums meet,
+// in the waves' order.  Each wave then has 16 rows of the result.  A CU's loads
+// bound it: 64 KiB a round of steps, 1.45 us, some 45 GB/s whatever the number
+// of CUs at work.  Fragments straight from memory into registers (8 waves, two
+// steps ahead, no spills) touch sixteen 64-byte pieces a load instead of eight
+// 128-byte lines: 44.7 us instead of 21.6 for [128, 5120] of 5120.
+// ---------------------------------------------------------------------------
+constexpr int kSplit = 4, kRing = 2;
+
+// The tile of a workgroup: XCD x takes a contiguous eighth, row tiles of a
+// column of tiles in a row, so that its part of B is read into one L2.
+template <int kOut, int kSF, typename E>
+__global__ __launch_bounds__(64 * kSplit) void mx_split_kernel(GemmArgs p) {
+    using O = std::conditional_t<kOut == 0, float, __bf16>;
+    constexpr int kCols = E::kGated ? 32 : 64;                  // results of a tile's row
+    constexpr int kRB = E::kGated ? 2 : 1;                      // scale runs of B
+    constexpr uint32_t kA = 0, kB = 8192, kS = 16384, kSlot = kS + 256u * (1 + kRB);
+    constexpr int kLoads = 16 + 1 + kRB;
+    constexpr int kPitch = 64 * 4 + 16;
+    constexpr uint32_t kSums = kSplit * 64 * 64 * 4;
+    static_assert(kSplit * kRing * kSlot <= 160 * 1024 && kSums + kSplit * 16 * kPitch <= kSplit * kRing * kSlot, "LDS");
+    static_assert((kRing - 1) * kLoads < 64, "vmcnt immediate");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kSplit * kRing * kSlot];
+
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3, tiles = p.tiles_m * p.tiles_n;
+    const uint32_t lo = uint32_t(uint64_t(tiles) * xcd / 8u), hi = uint32_t(uint64_t(tiles) * (xcd + 1u) / 8u);
+    if (lo + j >= hi) return;                                   // uniform
+    const uint32_t tn = (lo + j) / p.tiles_m, tm = lo + j - tn * p.tiles_m;
+    const int64_t m0 = int64_t(tm) * 64, n0 = int64_t(tn) * kCols;
+    const uint8_t *B = p.B, *sB = p.sB;
+    bool zero = false;
+    int32_t grp = 0;
+    if (p.offs != nullptr) {
+        group_ends(p, m0, &grp);
+        zero = grp >= p.G;
+        if (zero) grp = 0;
+        B += int64_t(grp) * p.b_gs;
+        sB += int64_t(grp) * p.sb_gs;
+    }
+    const uint32_t steps = zero ? 0u : uint32_t(p.K / kTile);
+    const uint32_t mine = steps > wave ? (steps - wave + kSplit - 1u) / kSplit : 0u;
+
+    const uint32_t lda = uint32_t(p.lda), ldb = uint32_t(p.ldb);
+    const uint32_t lr = lane >> 3, lc = (lane & 7u) ^ lr;
+    const uint32_t voa = lr * lda + 16u * lc, vob = lr * ldb + 16u * lc;
+    const v4i ra = pipe_rsrc(p.A + m0 * p.lda), rb = pipe_rsrc(B + n0 * p.ldb);
+    const v4i ru = pipe_rsrc(B + (n0 + (E::kGated ? p.e.up : 0)) * p.ldb);
+    // scales: the run of 64 rows that holds the tile's (gated: half of it)
+    constexpr bool kRowsForm = kSF == kScalesRows;
+    const int64_t b64 = n0 / 64 * 64, u64 = (n0 + (E::kGated ? p.e.up : 0)) / 64 * 64;
+    auto org = [&](int64_t row, int64_t rs) { return kSF == kScalesMfma ? (row / 64) * rs : kRowsForm ? row * rs : row; };
+    const v4i rs_a = pipe_rsrc(p.sA + org(m0, p.sa_rs)), rs_b = pipe_rsrc(sB + org(b64, p.sb_rs));
+    const v4i rs_u = pipe_rsrc(sB + org(u64, p.sb_rs));
+    const uint32_t step_a = kSF == kScalesMfma ? 256u : kRowsForm ? 4u : 4u * uint32_t(p.sa_bs);
+    const uint32_t step_b = kSF == kScalesMfma ? 256u : kRowsForm ? 4u : 4u * uint32_t(p.sb_bs);
+    auto lane_off = [&](int64_t rs, int64_t bs) {
+        return kSF == kScalesMfma ? 4u * lane : kRowsForm ? lane * uint32_t(rs) : (lane >> 4) * uint32_t(bs) + 4u * (lane & 15u);
+    };
+    const uint32_t vsa = lane_off(p.sa_rs, p.sa_bs), vsb = lane_off(p.sb_rs, p.sb_bs);
+    const uint32_t ring = uint32_t(reinterpret_cast<uintptr_t>(lds)) + wave * (kRing * kSlot);
+    auto issue = [&](uint32_t i, uint32_t slot) {
+        const uint32_t step = __builtin_amdgcn_readfirstlane(wave + kSplit * i), k = step * uint32_t(kTile), at = ring + slot * kSlot;
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+            if (E::kGated && q >= 4) pipe_load16_nt(ru, at + kB + 1024u * q, vob, 8u * (q - 4u) * ldb + k);
+            else pipe_load16_nt(rb, at + kB + 1024u * q, vob, 8u * q * ldb + k);
+        }
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) pipe_load16(ra, at + kA + 1024u * q, voa, 8u * q * lda + k);
+        pipe_load4(rs_a, at + kS, vsa, step * step_a);
+        pipe_load4(rs_b, at + kS + 256u, vsb, step * step_b);
+        if (E::kGated) pipe_load4(rs_u, at + kS + 512u, vsb, step * step_b);
+    };
+    v4f acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[i][n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (uint32_t i = 0; i < uint32_t(kRing); ++i)
+        if (i < mine) issue(i, i);
+    const uint32_t sel = plain_scale_sel<kSF == kScalesMfma ? kScalesRows : kSF>(lane), half = uint32_t(n0 >> 5) & 1u;
+    uint32_t slot = 0;
+    for (uint32_t i = 0; i < mine; ++i) {
+        // step i has arrived; near the end, where fewer are under way, all are waited for
+        if (i + kRing <= mine) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRing - 1) * kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint8_t* st = lds + wave * (kRing * kSlot) + slot * kSlot;
+        int sa[1], sb[1];
+        if constexpr (kSF == kScalesMfma) {
+            sa[0] = *reinterpret_cast<const int*>(st + kS + 4u * lane);
+            sb[0] = *reinterpret_cast<const int*>(st + kS + 256u + 4u * lane);
+            if (E::kGated) sb[0] = pair_scales(sb[0], *reinterpret_cast<const int*>(st + kS + 512u + 4u * lane), half);
+        } else {
+            uint32_t raw[4], rawb[4];
+            plain_scale_read<kSF>(st + kS, lane, raw);
+            plain_scale_read<kSF>(st + kS + 256u, lane, rawb);
+            sa[0] = plain_scale_pick(raw, sel);
+            sb[0] = plain_scale_pick(rawb, sel);
+            if (E::kGated) {
+                plain_scale_read<kSF>(st + kS + 512u, lane, raw);
+                sb[0] = pair_scales(sb[0], plain_scale_pick(raw, sel), half);
+            }
+        }
+        mma_step<4, 4>(acc, reinterpret_cast<const uint4*>(st + kA), reinterpret_cast<const uint4*>(st + kB), 0u, 0u, lane, sa, sb,
+                       std::make_integer_sequence<int, 4>{});
+        if (i + kRing < mine) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read
+            issue(i + kRing, slot);
+        }
+        slot = slot + 1u == uint32_t(kRing) ? 0u : slot + 1u;
+    }
+
+    // what the epilogue needs, while the sums meet
+    const float* add = bias_of<E>(p, grp);
+    float bias[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        bias[n] = add ? add[n0 + 16 * (E::kGated ? n % 2 : n) + (lane & 15u) + (E::kGated && n >= 2 ? p.e.up : 0)] : 0.f;
+    const int64_t row0 = m0 + 16 * int64_t(wave);
+    using R = EpRows<O, kCols>;
+    R rows;
+    const uint32_t left = uint32_t(p.N - n0);
+    if (p.e.residual) rows.read(p.e, row0, n0, 16u, left);
+    __syncthreads();                                             // every ring is read
+    float* sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            *reinterpret_cast<v4f*>(sums + ((wave * 16u + uint32_t(i) * 4u + n) * 64u + lane) * 4u) = acc[i][n];
+    __syncthreads();
+    uint8_t* ep = lds + kSums + wave * (16 * kPitch);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        v4f x = *reinterpret_cast<const v4f*>(sums + ((wave * 4u + n) * 64u + lane) * 4u);
+#pragma unroll
+        for (uint32_t w = 1; w < uint32_t(kSplit); ++w) x += *reinterpret_cast<const v4f*>(sums + ((w * 16u + wave * 4u + n) * 64u + lane) * 4u);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<float*>(ep + (4u * (lane >> 4) + v) * kPitch + (16u * n + (lane & 15u)) * 4u) = x[v] + bias[n];
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);                          // lgkmcnt(0)
+    __builtin_amdgcn_wave_barrier();
+    act_switch(p.e.act, [&](auto a) {
+        rows.template write<decltype(a)::value, E::kGated>(p.e, static_cast<O*>(p.C), p.ldc, ep, kPitch, row0, n0, 16u, left, zero);
+    });
+}
+
 // The plain scale form a view allows the pipelined kernel to load, or -1:
 // rows form (block stride 1, row stride a multiple of 4), blocks form (row
 // stride 1, block stride a multiple of 4); the base and the per-group stride
@@ -920,9 +1077,46 @@ int plain_scale_form(const uint8_t* s, int64_t rs, int64_t bs, int64_t K, int64_
     return -1;
 }
 
+// Which tiles a product with an epilogue takes: the form that splits the
+// contraction, 128 x 256 or (dense only) 256 x 256, by the time that rounds of
+// them on 256 CUs take, fixed and for each step of the contraction.  Measured
+// (us for the three; dense, bf16 results, K = 5120 but where said):
+//   [128, 128] K 512       5.2   13.0   16.8    [1024, 2048] K 2048  17.4  25.0  37.4
+//   [128, 5120]           21.8   47.4   66.0    [1024, 5120]         95.6  51.1  71.4
+//   [128, 14336] K 4096   32.7   44.4   60.8    [1024, 8192] K 8192   220  98.6   113
+//   [256, 5120]           36.2   47.8   70.0    [2048, 1024]         42.7  47.7  70.4
+//   [512, 2048]           19.1   47.8   70.0    [2048, 5120]          201  96.1  73.6
+//   [512, 5120]           50.3   48.7   70.4    [4096, 2048] K 512   34.0  14.8  21.8
+//   [768, 5120]           70.2   49.9   71.5    [4096, 4096] K 4096   239  87.8  70.8
+enum class Tiles { kSplit, kHalf, kWhole };
+template <typename E>
+Tiles tile_form(const GemmArgs& p) {
+    const int64_t W = E::kGated ? 2 * p.N : p.N, steps = p.K / kTile;
+    auto time = [&](int64_t tiles, double fixed, double step) { return double((tiles + 255) / 256) * (fixed + step * double(steps)); };
+    const double split = time(p.M / 64 * (W / 64), 3.0, 0.40), half = time(p.M / 128 * ((W + 255) / 256), 9.0, 0.95);
+    const double whole = p.offs ? 1e30 : time((p.M + 255) / 256 * ((W + 255) / 256), 11.0, 1.45);
+    return split <= half && split <= whole ? Tiles::kSplit : half <= whole ? Tiles::kHalf : Tiles::kWhole;
+}
+
+// Dense products with an epilogue in 128 x 256 tiles.
+template <int kSF, typename E>
+hipError_t launch_half(GemmArgs& p, int out_dtype, hipStream_t stream) {
+    using P = Pipe<4, 4, 2, 4>;
+    constexpr int kCols = E::kGated ? P::kTN / 2 : P::kTN;
+    p.tiles_m = uint32_t(p.M / P::kTM);
+    p.tiles_n = uint32_t((p.N + kCols - 1) / kCols);
+    const dim3 grid(p.tiles_m * p.tiles_n), block(P::kThreads);
+    if (out_dtype == 0) hipLaunchKernelGGL((mx_gemm_pipe_kernel<0, 4, 4, 2, 4, kSF, false, E>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((mx_gemm_pipe_kernel<1, 4, 4, 2, 4, kSF, false, E>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
 // Row groups: 128-row tiles (one group unit) of 8 waves; otherwise 256 x 256.
 template <int kSF, typename E>
 hipError_t launch_pipe(GemmArgs& p, int out_dtype, hipStream_t stream) {
+    if constexpr (E::kOn) {                                     // others keep the order of their sums
+        if (p.offs == nullptr && tile_form<E>(p) == Tiles::kHalf) return launch_half<kSF, E>(p, out_dtype, stream);
+    }
     if (p.mode == 0 && p.offs != nullptr) {
         // 128 x 256 tiles (a group unit is 128 rows).  Each XCD's share is at
         // most ceil(tiles_m / 8) + 1 row tiles (its covered range and its
@@ -950,6 +1144,16 @@ hipError_t launch_pipe(GemmArgs& p, int out_dtype, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int kSF, typename E>
+hipError_t launch_split(GemmArgs& p, int out_dtype, hipStream_t stream) {
+    p.tiles_m = uint32_t(p.M / 64);
+    p.tiles_n = uint32_t(p.N / (E::kGated ? 32 : 64));
+    const dim3 grid((p.tiles_m * p.tiles_n + 7u) / 8u * 8u), block(64 * kSplit);
+    if (out_dtype == 0) hipLaunchKernelGGL((mx_split_kernel<0, kSF, E>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((mx_split_kernel<1, kSF, E>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
 // The kernel that a call's operands allow.
 template <typename E>
 hipError_t launch_any(GemmArgs& p, int out_dtype, bool mfma_scales, hipStream_t stream) {
@@ -964,6 +1168,13 @@ hipError_t launch_any(GemmArgs& p, int out_dtype, bool mfma_scales, hipStream_t 
         const int fa = plain_scale_form(p.sA, p.sa_rs, p.sa_bs, p.K, 0);
         const int fb = plain_scale_form(p.sB, p.sb_rs, p.sb_bs, p.K, row_groups ? p.sb_gs : 0);
         sf = fa == fb ? fa : -1;
+    }
+    if constexpr (E::kOn) {
+        if (sf >= 0 && tile_form<E>(p) == Tiles::kSplit) {
+            if (sf == kScalesMfma) return launch_split<kScalesMfma, E>(p, out_dtype, stream);
+            if (sf == kScalesRows) return launch_split<kScalesRows, E>(p, out_dtype, stream);
+            return launch_split<kScalesBlocks, E>(p, out_dtype, stream);
+        }
     }
     if (sf >= 0 && rows16) {
         if (sf == kScalesMfma) return launch_pipe<kScalesMfma, E>(p, out_dtype, stream);
