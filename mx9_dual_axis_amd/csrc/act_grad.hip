@@ -10,10 +10,15 @@
 // One pass over dy and pre, which bounds it (HBM).  A workgroup takes a few
 // rows of one group (row tiles are numbered group by group, as the products
 // number theirs) by 32 pieces of 16 bytes: lane c of 32 holds the columns of
-// piece c, eight rows at a time, and adds its columns' sums in registers.  They
-// meet in LDS, and each row tile leaves its sums; a second kernel adds those
-// of a group's tiles in their order, so the same inputs give the same bits.
-// Row tiles are as tall as still gives every CU a few workgroups.
+// piece c, eight rows at a time, two of them in flight to a thread (four: no
+// faster, and half the waves fit), and adds its columns' sums in registers.
+// They meet in LDS, and each row tile leaves its sums; a second kernel adds
+// those of a group's tiles in their order, so the same inputs give the same
+// bits.  dy and pre are read for the last time, so they are loaded past the
+// caches: after other work, 16384 x 8192 bf16 GELU took 168 us so and 198 with
+// plain loads, and the read of dpre that follows is as fast or faster.  Its
+// tiles since (below): 141 us, 5.7 TB/s; gated SiLU over 64 groups, 20480 x
+// 2048: 73 us, 5.8 TB/s, and 13 more for the bias.
 #include "act.h"
 #include "mxq_kernels.h"
 
@@ -21,6 +26,7 @@ namespace mxq {
 namespace {
 
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+typedef u4 u4_at2 __attribute__((aligned(2)));
 
 struct GradArgs {
     const void *dy, *pre;
@@ -80,14 +86,14 @@ __device__ __forceinline__ void each_group(const GradArgs& p, F&& f) {
     }
 }
 
-constexpr int kCol = 32, kRow = 8, kThr = kCol * kRow;
+constexpr int kCol = 32, kRow = 8, kThr = kCol * kRow, kDeep = 2;
 
 template <typename T, bool kGated, int kAct>
 __device__ __forceinline__ void grad_rows(const GradArgs& p, int64_t m0, int64_t m1, bool zero, int64_t tile, float* lds) {
     constexpr int kPer = 16 / int(sizeof(T)), kParts = kGated ? 2 : 1;
     const uint32_t t = threadIdx.x, c = t & 31u, r = t >> 5;
     const int64_t col = (int64_t(blockIdx.y) * kCol + c) * kPer;
-    const bool some = col < p.N, all = col + kPer <= p.N;
+    const bool all = col + kPer <= p.N;
     const T *dy = static_cast<const T*>(p.dy) + col, *pre = static_cast<const T*>(p.pre) + col;
     T* out = static_cast<T*>(p.dpre) + col;
     float sum[kParts][kPer];
@@ -95,53 +101,86 @@ __device__ __forceinline__ void grad_rows(const GradArgs& p, int64_t m0, int64_t
     for (int h = 0; h < kParts; ++h)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) sum[h][i] = 0.f;
-    auto load = [&](const T* from, T (&v)[kPer]) {
-        if (all) {
-            __builtin_memcpy(v, from, 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) v[i] = from[min(int64_t(i), p.N - 1 - col)];
+    auto one = [&](float g, float x, float u, int i, float& a, float& b) {
+        float value;
+        a = g * act_slope<kAct>(x, &value);
+        if constexpr (kGated) {
+            a *= u;
+            b = g * value;
+            sum[1][i] += b;
         }
+        sum[0][i] += a;
     };
-    auto store = [&](T* to, const T (&v)[kPer]) {
-        if (all) {
-            u4 x;
-            __builtin_memcpy(&x, v, 16);
-            __builtin_memcpy(to, &x, 16);
-        } else {
+    struct Row {
+        u4 d, x, u;
+    };
+    auto piece = [](const T* from) { return __builtin_nontemporal_load(reinterpret_cast<const u4_at2*>(from)); };
+    auto fetch = [&](Row& w, int64_t m) {
+        w.d = piece(dy + m * p.ld_dy);
+        w.x = piece(pre + m * p.ld_pre);
+        if constexpr (kGated) w.u = piece(pre + m * p.ld_pre + p.N);
+    };
+    auto finish = [&](const Row& w, int64_t m) {
+        T d[kPer], x[kPer], u[kPer], o[kPer], ou[kPer];
+        __builtin_memcpy(d, &w.d, 16);
+        __builtin_memcpy(x, &w.x, 16);
+        if constexpr (kGated) __builtin_memcpy(u, &w.u, 16);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (col + i < p.N) to[i] = v[i];
+        for (int i = 0; i < kPer; ++i) {
+            float a, b = 0.f;
+            one(Elem<T>::get(d[i]), Elem<T>::get(x[i]), kGated ? Elem<T>::get(u[i]) : 0.f, i, a, b);
+            o[i] = Elem<T>::put(a);
+            if constexpr (kGated) ou[i] = Elem<T>::put(b);
         }
+        __builtin_memcpy(out + m * p.ld_d, o, 16);
+        if constexpr (kGated) __builtin_memcpy(out + m * p.ld_d + p.N, ou, 16);
     };
-    if (some) {
-        for (int64_t m = m0 + r; m < m1; m += kRow) {
-            T d[kPer], x[kPer], u[kPer], o[kPer], ou[kPer];
-            if (!zero) {
-                load(dy + m * p.ld_dy, d);
-                load(pre + m * p.ld_pre, x);
-                if (kGated) load(pre + m * p.ld_pre + p.N, u);
+    int64_t m = m0 + r;
+    if (zero) {
+        for (; m < m1; m += kRow) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (col + i >= p.N) continue;
+                out[m * p.ld_d + i] = Elem<T>::put(0.f);
+                if constexpr (kGated) out[m * p.ld_d + p.N + i] = Elem<T>::put(0.f);
+            }
+        }
+    } else if (all) {
+        // kDeep rows of the thread are read before the first is worked on
+        for (; m + (kDeep - 1) * kRow < m1; m += kDeep * kRow) {
+            Row w[kDeep];
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) fetch(w[i], m + i * kRow);
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                finish(w[i], m + i * kRow);
+            }
+        }
+        for (; m < m1; m += kRow) {
+            Row w;
+            fetch(w, m);
+            finish(w, m);
+        }
+    } else {
+        // the last piece of a row that ends inside it
+        for (; m < m1; m += kRow) {
+            T d[kPer], x[kPer], u[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (col + i >= p.N) continue;
+                d[i] = dy[m * p.ld_dy + i];
+                x[i] = pre[m * p.ld_pre + i];
+                if constexpr (kGated) u[i] = pre[m * p.ld_pre + p.N + i];
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                if (zero) {
-                    o[i] = ou[i] = Elem<T>::put(0.f);
-                    continue;
-                }
-                float value;
-                const float slope = act_slope<kAct>(Elem<T>::get(x[i]), &value), g = Elem<T>::get(d[i]);
-                float a = g * slope;
-                if (kGated) {
-                    a *= Elem<T>::get(u[i]);
-                    const float b = g * value;
-                    sum[kParts - 1][i] += b;
-                    ou[i] = Elem<T>::put(b);
-                }
-                sum[0][i] += a;
-                o[i] = Elem<T>::put(a);
+                if (col + i >= p.N) continue;
+                float a, b = 0.f;
+                one(Elem<T>::get(d[i]), Elem<T>::get(x[i]), kGated ? Elem<T>::get(u[i]) : 0.f, i, a, b);
+                out[m * p.ld_d + i] = Elem<T>::put(a);
+                if constexpr (kGated) out[m * p.ld_d + p.N + i] = Elem<T>::put(b);
             }
-            store(out + m * p.ld_d, o);
-            if (kGated) store(out + m * p.ld_d + p.N, ou);
         }
     }
     if (p.sums == nullptr || zero) return;                                  // uniform
@@ -188,10 +227,12 @@ __global__ __launch_bounds__(kThr) void act_grad_kernel(GradArgs p) {
     act_switch(p.act, [&](auto a) { grad_rows<T, kGated, decltype(a)::value>(p, m0, m1, zero, tile, lds); });
 }
 
-// The sums of one group's row tiles, for 64 channels: 16 segments of the tiles
-// in turn, then the segments.
-__global__ __launch_bounds__(1024) void bias_sum_kernel(GradArgs p, int64_t W) {
-    __shared__ float lds[16][64];
+// The sums of one group's row tiles for 64 channels: kSeg segments of the tiles
+// in turn, eight loads in flight, then the segments.  16 segments where groups
+// have many tiles, else four and smaller workgroups.
+template <int kSeg>
+__global__ __launch_bounds__(64 * kSeg) void bias_sum_kernel(GradArgs p, int64_t W) {
+    __shared__ float lds[kSeg][64];
     const uint32_t t = threadIdx.x, c = t & 63u, seg = t >> 6;
     const int32_t g = int32_t(blockIdx.y);
     int64_t first = 0, tiles = (p.M + (int64_t(1) << p.shift) - 1) >> p.shift;
@@ -205,29 +246,37 @@ __global__ __launch_bounds__(1024) void bias_sum_kernel(GradArgs p, int64_t W) {
             return true;
         });
     }
-    const int64_t n = int64_t(blockIdx.x) * 64 + c, per = (tiles + 15) / 16;
+    const int64_t n = int64_t(blockIdx.x) * 64 + c, per = (tiles + kSeg - 1) / kSeg;
     const int64_t b0 = min(int64_t(seg) * per, tiles), b1 = min(b0 + per, tiles);
+    const float* from = p.sums + first * W + min(n, W - 1);
     float s = 0.f;
-    if (n < W) {
-#pragma unroll 8
-        for (int64_t b = b0; b < b1; ++b) s += p.sums[(first + b) * W + n];
+    for (int64_t b = b0; b < b1; b += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = from[min(b + i, b1 - 1) * W];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += b + i < b1 ? v[i] : 0.f;
     }
     lds[seg][c] = s;
     __syncthreads();
-    if (seg == 0 && n < W) {
-        s = 0.f;
+    if (seg != 0 || n >= W) return;
+    s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) s += lds[w][c];
-        p.dbias[int64_t(g) * W + n] = s;
-    }
+    for (int w = 0; w < kSeg; ++w) s += lds[w][c];
+    p.dbias[int64_t(g) * W + n] = s;
 }
 
-// Rows of a tile: at least 16 and at most 256, while there are 1024 workgroups
-// (four to a CU).
+// Rows of a tile: at least 16 and at most 256, while there are 4096 workgroups
+// (16 to a CU: 16384 x 8192 bf16 took 161 us with half of them, 141 so; twice as
+// many cost 20480 x 2048 gated in 64 groups 8 us in the sums of the bias) or
+// 1024 row tiles (a bias adds one number of each).
 int grad_shift(int64_t M, int64_t N, int esz) {
     const int64_t slabs = (N * esz + 16 * kCol - 1) / (16 * kCol);
     int s = 8;
-    while (s > 4 && ((M + (int64_t(1) << s) - 1) >> s) * slabs < 1024) --s;
+    for (; s > 4; --s) {
+        const int64_t tiles = (M + (int64_t(1) << s) - 1) >> s;
+        if (tiles * slabs >= 4096 || tiles >= 1024) break;
+    }
     return s;
 }
 int64_t grad_tiles(int64_t M, int32_t G, bool groups, int shift) {
@@ -267,7 +316,11 @@ hipError_t launch_act_grad(const void* dy, int64_t ld_dy, const void* pre, int64
         if (e != hipSuccess) return e;
     }
     if (dbias) {
-        hipLaunchKernelGGL(bias_sum_kernel, dim3(uint32_t((W + 63) / 64), uint32_t(p.G)), dim3(1024), 0, stream, p, W);
+        const dim3 grid(uint32_t((W + 63) / 64), uint32_t(p.G));
+        if ((M >> p.shift) / p.G < 32)
+            hipLaunchKernelGGL((bias_sum_kernel<4>), grid, dim3(256), 0, stream, p, W);
+        else
+            hipLaunchKernelGGL((bias_sum_kernel<16>), grid, dim3(1024), 0, stream, p, W);
         return hipGetLastError();
     }
     return hipSuccess;
