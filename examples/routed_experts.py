@@ -12,6 +12,15 @@ autograd function over the library's forward and backward calls:
     Experts  mx_grouped_gemm_rows          mx_grouped_gemm_rows (rows), mx_grouped_gemm_k (weights)
     Combine  mx_combine          backward  mx_combine_grad
 
+With a balancing bias the layer is routed by sigmoid scores out of the better
+groups of experts, and the experts' first product forms silu(gate) up before
+its results leave the chip:
+
+    ScoredRoute   mx_route_scored           backward  mx_route_scored_grad
+    GatedExperts  mx_grouped_gemm_rows_act  backward  mx_act_grad, then as Experts
+
+and each step moves the bias towards even counts (mx_route_bias_step).
+
 The backward calls read the routing again, which the next mx_route on the same
 buffers writes over: each function notes the routing's generation and its
 backward refuses another one.  Micro-batches, or layers, that are alive at once
@@ -52,6 +61,27 @@ class Route(torch.autograd.Function):
         return dlogits, None, None
 
 
+SCORED = dict(score="sigmoid", groups=4, top_groups=2)
+
+
+class ScoredRoute(torch.autograd.Function):
+    """Route by scores and a balancing bias, which has no gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, plan, bias, valid):
+        ctx.save_for_backward(logits, valid)
+        ctx.plan = mxq.mx_route_scored(logits, bias=bias, valid=valid, out=plan, **SCORED)
+        ctx.generation = plan.generation
+        return plan.weight.clone(), plan.loss.clone()
+
+    @staticmethod
+    def backward(ctx, dweight, dloss):
+        logits, valid = ctx.saved_tensors
+        dlogits = mxq.mx_route_scored_grad(logits, ctx.plan, dweight.contiguous(), dloss.contiguous(), valid,
+                                           generation=ctx.generation)
+        return dlogits, None, None, None
+
+
 class Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
@@ -81,14 +111,39 @@ class Experts(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         ctx.plan.require(ctx.generation)
-        qt, st, wt, swt = ctx.saved_tensors
-        E, N, K = ctx.shape
-        offs = ctx.plan.offs
-        g, sg, gt, sgt = mxq.mx_quantize_grouped(dy.contiguous(), offs)
-        drows = mxq.mx_grouped_gemm_rows(g, sg, wt.view(K, E, N).permute(1, 0, 2), swt.view(E, N // 32, K).permute(0, 2, 1),
-                                         offs, torch.bfloat16)
-        dW = mxq.mx_grouped_gemm_k(gt, sgt.t(), qt, st.t(), offs, torch.bfloat16)
-        return drows, dW, None
+        return *products_grad(dy.contiguous(), *ctx.saved_tensors, ctx.shape, ctx.plan.offs), None
+
+
+def products_grad(dy, qt, st, wt, swt, shape, offs):
+    """(gradient of the rows, of the weights) of the experts' product."""
+    E, N, K = shape
+    g, sg, gt, sgt = mxq.mx_quantize_grouped(dy, offs)
+    drows = mxq.mx_grouped_gemm_rows(g, sg, wt.view(K, E, N).permute(1, 0, 2), swt.view(E, N // 32, K).permute(0, 2, 1),
+                                     offs, torch.bfloat16)
+    return drows, mxq.mx_grouped_gemm_k(gt, sgt.t(), qt, st.t(), offs, torch.bfloat16)
+
+
+class GatedExperts(torch.autograd.Function):
+    """rows [M, K], W [E, 2 H, K] -> silu(gate) up [M, H] in the product's
+    epilogue; what it was formed of is kept for the gradient."""
+
+    @staticmethod
+    def forward(ctx, rows, W, plan):
+        E, N, K = W.shape
+        q, s, qt, st = mxq.mx_quantize_grouped(rows, plan.offs)
+        w, sw, wt, swt = mxq.mx_quantize_2d_dual(W.reshape(E * N, K))
+        y, pre = mxq.mx_grouped_gemm_rows_act(q, s, w.view(E, N, K), sw.view(E, N, K // 32), plan.offs, act="silu",
+                                              gated=True, pre=True)
+        ctx.save_for_backward(qt, st, wt, swt, pre)
+        ctx.plan, ctx.generation, ctx.shape = plan, plan.generation, (E, N, K)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        ctx.plan.require(ctx.generation)
+        *operands, pre = ctx.saved_tensors
+        dpre, _ = mxq.mx_act_grad(dy.contiguous(), pre, "silu", True, ctx.plan.offs, bias=False)
+        return *products_grad(dpre, *operands, ctx.shape, ctx.plan.offs), None
 
 
 class Combine(torch.autograd.Function):
@@ -111,13 +166,17 @@ def gated(a):
     return F.silu(gate) * up
 
 
-def train_layer(x, params, plan, valid=None):
+def train_layer(x, params, plan, valid=None, bias=None):
     """x bf16 [T, K] -> (y bf16 [T, K], balance loss).  `plan` is this pass's
-    until its backward is done."""
+    until its backward is done.  bias: float32 [E], for routing by scores."""
     router, W1, W2 = params
-    weight, balance = Route.apply(x.float() @ router.t(), plan, valid)
-    rows = Dispatch.apply(x, plan)
-    h = gated(Experts.apply(rows, W1.bfloat16(), plan))
+    logits = x.float() @ router.t()
+    if bias is None:
+        weight, balance = Route.apply(logits, plan, valid)
+        h = gated(Experts.apply(Dispatch.apply(x, plan), W1.bfloat16(), plan))
+    else:
+        weight, balance = ScoredRoute.apply(logits, plan, bias, valid)
+        h = GatedExperts.apply(Dispatch.apply(x, plan), W1.bfloat16(), plan)
     return Combine.apply(Experts.apply(h.contiguous(), W2.bfloat16(), plan), weight, plan), balance
 
 
@@ -133,10 +192,10 @@ def init(E, K, H, device, seed=0):
 class Server:
     """The layer with int8 experts for batches of T tokens, as a graph."""
 
-    def __init__(self, params, T, k, device):
+    def __init__(self, params, T, k, device, bias=None):
         router, W1, W2 = (p.detach() for p in params)
         E, H2, K = W1.shape
-        self.router = router
+        self.router, self.bias = router, bias
         q, s = mxq.i8_quantize_rows(W1.reshape(E * H2, K))
         self.W1, self.s1 = q.view(E, H2, K), s.view(E, H2)
         q, s = mxq.i8_quantize_rows(W2.reshape(E * K, H2 // 2))
@@ -153,9 +212,16 @@ class Server:
             self.y = self.step(self.x)
 
     def step(self, x):
-        plan = mxq.mx_route(x.float() @ self.router.t(), out=self.plan)
+        logits = x.float() @ self.router.t()
+        if self.bias is None:
+            plan = mxq.mx_route(logits, out=self.plan)
+        else:
+            plan = mxq.mx_route_scored(logits, bias=self.bias, out=self.plan, **SCORED)
         q, s = mxq.mx_dispatch_i8(x, plan.slot, plan.src)
-        h = gated(mxq.i8_grouped_gemm_rows(q, s, self.W1, self.s1, plan.offs, torch.bfloat16))
+        if self.bias is None:
+            h = gated(mxq.i8_grouped_gemm_rows(q, s, self.W1, self.s1, plan.offs, torch.bfloat16))
+        else:
+            h = mxq.i8_grouped_gemm_rows_act(q, s, self.W1, self.s1, plan.offs, act="silu", gated=True)
         q, s = mxq.i8_quantize_rows(h)
         return mxq.mx_combine(mxq.i8_grouped_gemm_rows(q, s, self.W2, self.s2, plan.offs, torch.bfloat16), plan.slot,
                               plan.weight)
@@ -166,13 +232,14 @@ class Server:
         return self.y
 
 
-def main(T=2048, E=16, K=512, H=256, k=2, steps=60, device="cuda:0"):
+def main(T=2048, E=16, K=512, H=256, k=2, steps=60, device="cuda:0", scored=False):
     """Train a layer back to the one it is a disturbed copy of, then serve it;
     returns the losses and the served outputs' distance from the trained
-    layer's."""
+    layer's.  scored: routed by scores with a balancing bias."""
     target = init(E, K, H, device, 2)
     params = [(p + 0.25 * d).detach().requires_grad_() for p, d in zip(target, init(E, K, H, device, 1))]
     plan = mxq.mx_routing(T, E, k, align=128, device=device)
+    bias = torch.zeros(E, device=device) if scored else None
     opt = torch.optim.Adam(params, lr=1e-3)
     g = torch.Generator(device=device)
     g.manual_seed(3)
@@ -180,21 +247,23 @@ def main(T=2048, E=16, K=512, H=256, k=2, steps=60, device="cuda:0"):
     for _ in range(steps):
         x = torch.randn((T, K), generator=g, device=device).bfloat16()
         with torch.no_grad():
-            want = train_layer(x, target, plan)[0].float()
-        y, balance = train_layer(x, params, plan)
+            want = train_layer(x, target, plan, bias=bias)[0].float()
+        y, balance = train_layer(x, params, plan, bias=bias)
         loss = F.mse_loss(y.float(), want) / want.square().mean()
         opt.zero_grad()
         (loss + 0.01 * balance.sum()).backward()
         opt.step()
+        if scored:
+            mxq.mx_route_bias_step(bias, plan.counts, 1e-3, out=bias)
         losses.append(float(loss.detach()))
-    print(f"trained {steps} steps: loss {losses[0]:.3f} -> {losses[-1]:.3f}, tokens per expert "
+    print(f"trained {steps} steps{' by scores' if scored else ''}: loss {losses[0]:.3f} -> {losses[-1]:.3f}, tokens per expert "
           f"{int(plan.counts.min())} to {int(plan.counts.max())}", flush=True)
     dist = {}
     for n in (1, 16, T):
         x = torch.randn((n, K), generator=g, device=device).bfloat16()
-        serve = Server(params, n, k, device)
+        serve = Server(params, n, k, device, bias)
         with torch.no_grad():
-            want = train_layer(x, params, mxq.mx_routing(n, E, k, align=128, device=device))[0].float()
+            want = train_layer(x, params, mxq.mx_routing(n, E, k, align=128, device=device), bias=bias)[0].float()
         got = serve(x).float()
         dist[n] = float((got - want).norm() / want.norm())
         torch.cuda.synchronize(device)
@@ -209,3 +278,4 @@ def main(T=2048, E=16, K=512, H=256, k=2, steps=60, device="cuda:0"):
 
 if __name__ == "__main__":
     main()
+    main(scored=True)

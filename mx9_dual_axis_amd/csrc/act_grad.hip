@@ -137,7 +137,13 @@ __device__ __forceinline__ void grad_rows(const GradArgs& p, int64_t m0, int64_t
     };
     int64_t m = m0 + r;
     if (zero) {
+        const u4 o = {};
         for (; m < m1; m += kRow) {
+            if (all) {
+                __builtin_memcpy(out + m * p.ld_d, &o, 16);
+                if constexpr (kGated) __builtin_memcpy(out + m * p.ld_d + p.N, &o, 16);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 if (col + i >= p.N) continue;
