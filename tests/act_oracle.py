@@ -12,6 +12,15 @@ result unless said:
   * gelu_tanh: its argument t within 6 u: 6 |t| u of the logistic, and silu's.
   * e^x below 2^-126 may be 0: results below 2^-118 may be, and a slope may lack
     2^-126 of what its logistic or density is multiplied by.
+Values that are rounded to bf16 next are formed in fewer operations (`brief`):
+  * e^x = 2^(x c), c = fp32(log2 e) (off by 0.25 u): the product's rounding and
+    c's move the argument by 1.25 u |x| log2 e, the result by 1.25 |x| u; 2 |x| u
+    are allowed.  Where it passes 2^126, so that its reciprocal may be 0, the
+    value is below 89 2^-126 < 2^-118.
+  * gelu: a polynomial fitted within 1.22e-5, its terms adding up to 1.6 of its
+    value: the 80 u above hold for its evaluation; x^2 and its two products with
+    constants' roundings: 4 u of x^2 / 2 at most.  1.3e-5 + 80 u + 2 x^2 u.
+  * gelu_tanh: its argument within 6 u + 2 u, times |t|: 8 |t| u, as above.
 Slopes alike, of the magnitudes of their two terms.  No activation is steeper
 than 1.13.
 """
@@ -42,12 +51,12 @@ def act(x, name):
     return x
 
 
-def evaluation(x, name):
+def evaluation(x, name, brief=False):
     """Relative error of an activation."""
     if name == "silu":
-        return torch.full_like(x, 16 * U)
+        return 16 * U + (2 * U * x.abs() if brief else torch.zeros_like(x))
     if name == "gelu":
-        return torch.full_like(x, 80 * U)
+        return 80 * U + (1.3e-5 + 2 * U * x * x if brief else torch.zeros_like(x))
     if name == "gelu_tanh":
         return (24 + 8 * (C * (x + 0.044715 * x ** 3)).abs()) * U
     return torch.zeros_like(x)
@@ -70,17 +79,18 @@ def slope(x, name):
     return torch.ones_like(x), torch.zeros_like(x)
 
 
-def epilogue(x, ex, name, gated, residual=None):
-    """(y, its error before the output's rounding) for x within ex."""
+def epilogue(x, ex, name, gated, residual=None, brief=False):
+    """(y, its error before the output's rounding) for x within ex; brief: the
+    output is bf16."""
     if gated:
         n = x.shape[1] // 2
         g, u, eg, eu = x[:, :n], x[:, n:], ex[:, :n], ex[:, n:]
         a = act(g, name)
-        ea = 1.2 * eg + evaluation(g, name) * a.abs() + TINY
+        ea = 1.2 * eg + evaluation(g, name, brief) * a.abs() + TINY
         y, e = a * u, ea * (u.abs() + eu) + a.abs() * eu + U * (a * u).abs()
     else:
         y = act(x, name)
-        e = 1.2 * ex + evaluation(x, name) * y.abs() + TINY
+        e = 1.2 * ex + evaluation(x, name, brief) * y.abs() + TINY
     if residual is not None:
         y = y + residual
         e = e + U * (y.abs() + e)

@@ -88,7 +88,7 @@ def test_dense_in_every_form(i, out, gated):
     wide = torch.randn((M, N + 5), generator=g, device=DEV).to(DT[out])
     res = wide[:, 2:N + 2] if has_res else None
     x, ex = sums8(a, sa, b, sb, bias)
-    want, err = ao.epilogue(x, ex, act, gated, None if res is None else res.double())
+    want, err = ao.epilogue(x, ex, act, gated, None if res is None else res.double(), out == "bf16")
     A, B = (a, b) if pieces else (at_any_byte(a), at_any_byte(b))
     mxq.i8_gemm_nt_act(A, sa, B, sb, bias, act, gated, res, out=buf[:, :N])
     near(buf[:, :N], want, err, "pitched result")
@@ -113,7 +113,7 @@ def test_by_expert_in_every_form(i, out, gated):
     want, err = (torch.zeros((M, N), dtype=torch.float64, device=DEV) for _ in range(2))
     for e, (r0, r1) in enumerate(ro.group_ranges(offs, M)):
         x, ex = sums8(a[r0:r1], sa[r0:r1], b[e], sb[e], None if bias is None else bias[e])
-        want[r0:r1], err[r0:r1] = ao.epilogue(x, ex, act, gated)
+        want[r0:r1], err[r0:r1] = ao.epilogue(x, ex, act, gated, None, out == "bf16")
     sa[offs[-1]:] = float("nan")                          # the tail is no group's
     od = torch.from_numpy(offs.astype(np.int32)).to(DEV)
     A, B = (a, b) if pieces else (at_any_byte(a), at_any_byte(b))
@@ -140,10 +140,11 @@ def test_linear(M, N, K, dtype, gated):
     for i, act in enumerate(ao.ACTS):
         res = torch.randn((M, N), generator=g, device=DEV).to(DT[dtype]) if i % 2 else None
         bi = bias if i != 2 else None
-        want, err = ao.epilogue(*sums8(q, s, b, sb, bi), act, gated, None if res is None else res.double())
+        of = (*sums8(q, s, b, sb, bi), act, gated, None if res is None else res.double())
+        want, err = ao.epilogue(*of, dtype == "bf16")
         near(mxq.i8_linear_act(x, b, sb, bi, act, gated, res), want, err, act)
         got = mxq.i8_linear_act(x, b, sb, bi, act, gated, None if res is None else res.float(), out_dtype=torch.float32)
-        near(got, want, err, f"{act}, fp32")
+        near(got, *ao.epilogue(*of), f"{act}, fp32")
 
 
 def test_without_an_epilogue_the_bits_are_those_of_the_product():
@@ -263,7 +264,7 @@ def test_mx_dense(M, N, K, out, gated):
         res = torch.randn((M, N + 1), generator=g, device=DEV).to(DT[out])[:, 1:] if i % 2 else None
         x = A.v @ B.v.t().contiguous() + (0 if bi is None else bi.double())
         ex = U * x.abs()
-        want, err = ao.epilogue(x, ex, act, gated, None if res is None else res.double())
+        want, err = ao.epilogue(x, ex, act, gated, None if res is None else res.double(), out == "bf16")
         call = mxq.mx_gemm_nt_act_mfma if form == "mfma" else mxq.mx_gemm_nt_act
         ops = (A.q, A.scales(form), B.q, B.scales(form))
         call(*ops, bi, act, gated, res, out=buf[:, :N], pre=kept[:, :W])
@@ -291,7 +292,7 @@ def test_mx_by_expert(sizes, tail, N, K, out, gated, form):
     x = torch.zeros((M, W), dtype=torch.float64, device=DEV)
     for e, (r0, r1) in enumerate(ro.group_ranges(ends, M)):
         x[r0:r1] = A.v[r0:r1] @ B.v[e].t().contiguous() + bias[e].double()
-    want, err = ao.epilogue(x, U * x.abs(), "silu", gated)
+    want, err = ao.epilogue(x, U * x.abs(), "silu", gated, None, out == "bf16")
     want[ends[-1]:] = 0
     call = mxq.mx_grouped_gemm_rows_act_mfma if form == "mfma" else mxq.mx_grouped_gemm_rows_act
     y, pre = call(A.q, A.scales(form), B.q, B.scales(form), offs, bias, "silu", gated, out_dtype=DT[out], pre=True)
