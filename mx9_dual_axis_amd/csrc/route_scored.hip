@@ -85,15 +85,17 @@ struct Score {
 };
 
 // e^x in binary64, within a few ulp: 2^n e^r, |r| <= ln 2 / 2, by 14 terms of the
-// series from the last (r^14 / 14! < 2^-54).  In a loop, for its few registers:
-// a polynomial's constants would be held through the whole kernel.
-__device__ __forceinline__ double exact_exp(double x) {
+// series (r^14 / 14! < 2^-54).  A function of its own: inlined six times its
+// constants take the registers of a wave, and the code, which most blocks fetch
+// once, is longer (16384 x 256, 8 groups: 40.1 us instead of 37.9).
+__device__ __attribute__((noinline)) double exact_exp(double x) {
+    constexpr double kFactorial[14] = {1, 1, 2, 6, 24, 120, 720, 5040, 40320, 362880, 3628800, 39916800, 479001600, 6227020800.};
     x = fmax(fmin(x, 1000.0), -1000.0);
     const double n = rint(x * 1.4426950408889634);
     const double r = fma(-n, 2.3190468138462996e-17, fma(-n, 0.6931471805599453, x));    // ln 2 in two parts
-    double s = 1.0;
-#pragma unroll 1
-    for (int i = 14; i >= 1; --i) s = fma(s, r / double(i), 1.0);
+    double s = 1.0 / 87178291200.;
+#pragma unroll
+    for (int i = 13; i >= 0; --i) s = fma(s, r, 1.0 / kFactorial[i]);
     return ldexp(s, int(n));
 }
 
