@@ -105,7 +105,7 @@ int mx_call(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int
     // The products' own checks, of W channels: C's pitch counts beyond its N
     // results, and an N that is not whole tiles is refused as such a W.
     int rc = check_gemm(A, lda, sA, sa_rs, sa_bs, B, ldb, sB, sb_rs, sb_bs, M, N % 128 == 0 ? W : 1, K, C,
-                        ldc < N ? -1 : ldc + (W - N), out_dtype, mfma);
+                        ldc < N || ldc > kMaxGemm ? -1 : ldc + (W - N), out_dtype, mfma);
     if (rc != MX_OK) return rc;
     if (groups && (G < 1 || G > (1 << 20))) return MX_E_SHAPE;
     if (!gemm_grid_fits(M, W, G, groups, false)) return MX_E_SHAPE;     // (smaller tiles are taken where they are few)

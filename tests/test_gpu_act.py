@@ -301,6 +301,33 @@ def test_mx_by_expert(sizes, tail, N, K, out, gated, form):
     assert not y[ends[-1]:].any() and not pre[ends[-1]:].any()
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_bias_that_experts_share_and_experts_without_rows(gated):
+    """70 groups of a stack of 73 experts; the bias by a pitch of 0, by one that
+    is wider than its rows, and contiguous: the same bits."""
+    g = gen(70 + gated)
+    E, G, N, K = 73, 70, 128, 128
+    W = 2 * N if gated else N
+    sizes = np.array([128 * (e % 3 == 0) for e in range(G)])
+    offs = torch.from_numpy(np.cumsum(sizes).astype(np.int32)).to(DEV)
+    M = int(sizes.sum()) + 128
+    one = torch.randn(W, generator=g, device=DEV)
+    wide = torch.full((E, W + 5), float("nan"), device=DEV)
+    wide[:, :W] = one
+    A, B = Operand((M, K), g, K), Operand((E, W, K), g, K)
+    qa, sa = mxq.i8_quantize_rows(torch.randn((M, K), generator=g, device=DEV))
+    qb, sb = mxq.i8_quantize_rows(torch.randn((E * W, K), generator=g, device=DEV) * K ** -0.5)
+    qb, sb = qb.view(E, W, K), sb.view(E, W)
+    calls = (lambda b: mxq.mx_grouped_gemm_rows_act(A.q, A.scales("rows"), B.q, B.scales("rows"), offs, b, "silu", gated),
+             lambda b: mxq.i8_grouped_gemm_rows_act(qa, sa, qb, sb, offs, b, "silu", gated))
+    for call in calls:
+        want = call(one.repeat(E, 1))
+        assert want[:M - 128].any(1).all() and not want[M - 128:].any()
+        assert torch.equal(call(one.expand(E, W)), want)
+        assert torch.equal(call(wide[:, :W]), want)
+        assert torch.equal(call(one.repeat(G, 1)), want)
+
+
 def test_mx_without_a_contraction_is_refused():
     """As mx_gemm_nt's: torch's empty operands have no address."""
     q, s = torch.empty((128, 0), dtype=torch.uint8, device=DEV), torch.empty((128, 0), dtype=torch.uint8, device=DEV)
@@ -334,7 +361,7 @@ def sum_error(d, e, rows, tiles):
 @pytest.mark.parametrize("act", ao.ACTS)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("M,N", [(1, 1), (3, 9), (17, 513), (333, 1111), (4100, 264)])
+@pytest.mark.parametrize("M,N", [(1, 1), (3, 9), (17, 513), (333, 1111), (4100, 264), (270001, 8)])
 def test_gradient(M, N, dtype, gated, act):
     g = gen(M + N)
     W = 2 * N if gated else N
@@ -355,7 +382,7 @@ def test_gradient(M, N, dtype, gated, act):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N", [8, 301])
 @pytest.mark.parametrize("sizes,tail", [([0, 3, 16, 1, 0, 40, 17, 15], 4), ([0, 0], 5), ([1000, 0, 257], 0), ([5] * 130, 7),
-                                        ([7, 0, 700] * 50, 100)])
+                                        ([7, 0, 700] * 50, 100), ([900, 0, 3000], 30)])
 def test_gradient_by_expert(sizes, tail, N, dtype, gated):
     g = gen(sum(sizes) + N)
     M, G, W = sum(sizes) + tail, len(sizes), 2 * N if gated else N
@@ -395,6 +422,33 @@ def test_slopes_at_the_ends():
         low = 1.0 if act == "none" else 0.0
         assert d[0, :8].tolist() == [1, 1, 1, zero, zero, low, low, low], act
         assert (d[0, 8].item() == 1) if act == "none" else d[0, 8].isnan(), act
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_rows_far_apart(gated):
+    """Results, residuals and kept sums 2^23 elements apart, 384 rows: offsets
+    past 32 bits.  The bits are those of contiguous rows."""
+    g = gen(23 + gated)
+    M, N, K, far = 384, 256, 256, 1 << 23
+    W = 2 * N if gated else N
+    bf = torch.bfloat16
+    out, res, kept, dpre = (torch.empty((M, far), dtype=bf, device=DEV)[:, 7:n + 7] for n in (N, N, W, W))
+    bias = torch.randn(W, generator=g, device=DEV)
+    near_res = torch.randn((M, N), generator=g, device=DEV).to(bf)
+    res.copy_(near_res)
+    A, B = Operand((M, K), g, K), Operand((W, K), g, K)
+    qa, sa = mxq.i8_quantize_rows(torch.randn((M, K), generator=g, device=DEV))
+    qb, sb = mxq.i8_quantize_rows(torch.randn((W, K), generator=g, device=DEV))
+    want = mxq.i8_gemm_nt_act(qa, sa, qb, sb, bias, "gelu", gated, near_res)
+    assert torch.equal(mxq.i8_gemm_nt_act(qa, sa, qb, sb, bias, "gelu", gated, res, out=out), want)
+    for form in ("rows", "odd"):
+        ops = (A.q, A.scales(form), B.q, B.scales(form), bias, "silu", gated)
+        want, pre = mxq.mx_gemm_nt_act(*ops, near_res, pre=True)
+        mxq.mx_gemm_nt_act(*ops, res, out=out, pre=kept)
+        assert torch.equal(out, want) and torch.equal(kept, pre)
+    want, sums = mxq.mx_act_grad(near_res, pre, "silu", gated)
+    _, got = mxq.mx_act_grad(res, kept, "silu", gated, out=(dpre, None))
+    assert torch.equal(dpre, want) and torch.equal(got, sums)
 
 
 # ---------------------------------------------------------- streams and graphs

@@ -300,6 +300,24 @@ def test_the_bias_evens_the_counts():
     assert sum(spread[-20:]) < 0.25 * sum(spread[:20])
 
 
+def test_logits_far_apart():
+    """Rows 2^23 elements apart: offsets past 32 bits, the bits of contiguous rows."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(23)
+    T, E, k = 300, 64, 4
+    z = torch.randn((T, E), generator=g, device=DEV).bfloat16()
+    far, out = (torch.empty((T, 1 << 23), dtype=torch.bfloat16, device=DEV)[:, 5:E + 5] for _ in range(2))
+    far.copy_(z)
+    bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+    dw = torch.randn((T, k), generator=g, device=DEV)
+    a, b = (mxq.mx_route_scored(x, k, bias, groups=4, top_groups=2) for x in (z, far))
+    for name in ("idx", "weight", "slot", "src", "counts", "offs", "live", "prob", "loss"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    want = mxq.mx_route_scored_grad(z, a, dw, torch.ones(1, device=DEV))
+    mxq.mx_route_scored_grad(far, b, dw, torch.ones(1, device=DEV), out=out)
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------------- state, graphs, refusals
 def test_routings_are_told_apart():
     z = torch.randn((40, 16), device=DEV)
