@@ -29,6 +29,12 @@
 // their binary64 values, a lane to each or two; where it is groups that are
 // close, or more than 32 experts, the four tokens of the wave are decided again
 // in binary64 from the logits in LDS, pick by pick.
+//
+// Bound by vector instructions: 131072 x 256 fp32 by sigmoid scores, a bias and
+// 8 groups take 117 us, of which 28 go to the tokens decided again (after the
+// pass, so that what they need takes no registers from the others: within it,
+// 301 us); without groups the call takes 102 us instead of 131.  A round of four
+// tokens is 1428 instructions; they fill half of the cycles.
 #include "act.h"
 #include "route_device.h"
 
@@ -748,7 +754,8 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
 //   softmax: dlogits = s (a - sum a s) - s sum_j d_j s_j, + d_j s_j at idx_j
 //
 // One pass, as route.hip's gradient: a row is in registers between its scores
-// and the result.
+// and the result.  131072 x 256 fp32: 62 us, 4.3 TB/s; the vector instructions
+// fill 62% of the cycles.
 struct ScoredGradArgs {
     const void* logits;
     int64_t ld;
