@@ -31,10 +31,11 @@
 // in binary64 from the logits in LDS, pick by pick.
 //
 // Bound by vector instructions: 131072 x 256 fp32 by sigmoid scores, a bias and
-// 8 groups take 117 us, of which 28 go to the tokens decided again (after the
-// pass, so that what they need takes no registers from the others: within it,
-// 301 us); without groups the call takes 102 us instead of 131.  A round of four
-// tokens is 1428 instructions; they fill half of the cycles.
+// 8 groups take 117 us (the call 128; without groups 101).  A round of four
+// tokens is 1428 instructions; they fill half of the cycles.  Tokens are decided
+// again after the pass, so that what they need takes no registers from the
+// others (within it the call took 301 us).  They are few, about one in 1500 here,
+// but a block waits some 10 us for one: without that code the call takes 105 us.
 #include "act.h"
 #include "route_device.h"
 
@@ -734,8 +735,10 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
                 for (int32_t i = on ? skip : todo - 1; i > 0; --i) bits &= bits - 1ull;
                 const uint32_t tok = uint32_t(__builtin_ctzll(bits));
                 const int64_t row = first + tok;
+                __builtin_amdgcn_s_setprio(3);                              // the block waits for this wave
                 decide_again<L, V>(p, a, logits + row * p.ld, redo[tok], stash[grp], bias, lists[grp], row, tok, on, pick, mask);
             }
+            __builtin_amdgcn_s_setprio(0);
             __syncthreads();
             if (t == 0) again = 0;
         }
