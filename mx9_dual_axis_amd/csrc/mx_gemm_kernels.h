@@ -576,10 +576,88 @@ __device__ int32_t group_ends(const GemmArgs& p, int64_t row, int32_t* group) {
     return c_carry;
 }
 
+// Row tiles of up to two units (256 rows) of one group, for 256 x 256 tiles:
+// XCD x takes a contiguous range of the groups' row tiles and its share of the
+// tail's, as above.  Tile lr of the XCD's: its first row, its rows (128 or 256)
+// and its group (G: the tail); false past the XCD's share.
+__device__ __forceinline__ bool pair_tile(const GemmArgs& p, uint32_t xcd, uint32_t lr, int64_t* m0, uint32_t* rows,
+                                          int32_t* group) {
+    const uint32_t lane = threadIdx.x & 63u;
+    const int32_t units = int32_t(p.M / 128);
+    // f(group, first unit, end, row tiles before it, its own) of 64 groups at a time
+    int32_t end = 0, tiles = 0;
+    auto scan = [&](auto&& f) {
+        end = tiles = 0;
+        for (int32_t base = 0; base < p.G; base += 64) {
+            const int32_t g = base + int32_t(lane);
+            int32_t c = g < p.G ? min(max(p.offs[g], 0) / 128, units) : 0;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int32_t o = __shfl_up(c, d, 64);
+                if (lane >= uint32_t(d)) c = max(c, o);
+            }
+            c = max(c, end);
+            int32_t start = __shfl_up(c, 1, 64);
+            if (lane == 0) start = end;
+            const int32_t own = (c - start + 1) / 2;
+            int32_t sum = own;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int32_t o = __shfl_up(sum, d, 64);
+                if (lane >= uint32_t(d)) sum += o;
+            }
+            if (f(g, start, c, tiles + sum - own, own)) return;
+            tiles += uniform(__shfl(sum, 63, 64));
+            end = uniform(__shfl(c, 63, 64));
+        }
+    };
+    scan([](int32_t, int32_t, int32_t, int32_t, int32_t) { return false; });
+    const uint32_t covered = uint32_t(tiles), tail = uint32_t(units - end + 1) / 2;
+    const uint32_t c0 = covered * xcd / 8u, c1 = covered * (xcd + 1u) / 8u;
+    const uint32_t t0 = tail * xcd / 8u, t1 = tail * (xcd + 1u) / 8u;
+    if (lr >= c1 - c0) {
+        const uint32_t z = t0 + (lr - (c1 - c0));
+        if (z >= t1) return false;
+        *m0 = int64_t(end) * 128 + int64_t(z) * 256;
+        *rows = uint32_t(min(p.M - *m0, int64_t(256)));
+        *group = p.G;
+        return true;
+    }
+    const int32_t at = int32_t(c0 + lr);
+    scan([&](int32_t g, int32_t start, int32_t c, int32_t before, int32_t own) {
+        const uint64_t mine = __ballot(before <= at && at < before + own);
+        if (mine == 0) return false;
+        const int w = __builtin_ctzll(mine);
+        const int32_t u = uniform(__shfl(start, w, 64)) + 2 * (at - uniform(__shfl(before, w, 64)));
+        *m0 = int64_t(u) * 128;
+        *rows = 128u * uint32_t(min(uniform(__shfl(c, w, 64)) - u, 2));
+        *group = uniform(__shfl(g, w, 64));
+        return true;
+    });
+    return true;
+}
+
+// Zeros in rows x cols elements, by kThr threads.
+template <typename O, int kThr>
+__device__ __forceinline__ void clear_rows(O* to, int64_t ld, uint32_t rows, uint32_t cols) {
+    constexpr uint32_t kPer = 16u / sizeof(O);
+    const bool whole = reinterpret_cast<uintptr_t>(to) % 16 == 0 && ld % kPer == 0;
+    const uint32_t pieces = (cols + kPer - 1u) / kPer;
+    for (uint32_t i = threadIdx.x; i < rows * pieces; i += uint32_t(kThr)) {
+        const uint32_t row = i / pieces, col = i % pieces * kPer;
+        O* at = to + int64_t(row) * ld + col;
+        if (whole && col + kPer <= cols) {
+            __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4*>(at));
+        } else {
+            for (uint32_t q = 0; q < kPer && col + q < cols; ++q) at[q] = O(0.f);
+        }
+    }
+}
+
 // A wave's results with an epilogue: 16 rows at a time through LDS in fp32.
 template <typename O, int MS, int NS, typename E>
 __device__ __forceinline__ void mx_store_act(const GemmArgs& p, const v4f (&acc)[MS][NS], uint8_t* lds, int64_t row0,
-                                             int64_t n0, uint32_t wn, uint32_t wave, int32_t grp, bool zero) {
+                                             int64_t m_end, int64_t n0, uint32_t wn, uint32_t wave, int32_t grp) {
     constexpr int kPitch = 16 * NS * 4 + 16, kCols = E::kGated ? 8 * NS : 16 * NS;
     using R = EpRows<O, kCols>;
     const uint32_t lane = threadIdx.x & 63u;
@@ -592,7 +670,7 @@ __device__ __forceinline__ void mx_store_act(const GemmArgs& p, const v4f (&acc)
         const int64_t col = col0 + 16 * (E::kGated ? j % (NS / 2) : j) + (lane & 15u);
         bias[j] = add && cols > 0 ? add[(E::kGated && j >= NS / 2 ? p.e.up : 0) + min(col, p.N - 1)] : 0.f;
     }
-    auto left = [&](int i) { return uint32_t(min(max(p.M - row0 - 16 * i, int64_t(0)), int64_t(16))); };
+    auto left = [&](int i) { return uint32_t(min(max(m_end - row0 - 16 * i, int64_t(0)), int64_t(16))); };
     R now;
     if (R::kAhead && p.e.residual) now.read(p.e, row0, col0, left(0), cols);
     __syncthreads();                                            // the stages are free
@@ -614,7 +692,7 @@ __device__ __forceinline__ void mx_store_act(const GemmArgs& p, const v4f (&acc)
         __builtin_amdgcn_wave_barrier();
         act_switch(p.e.act, [&](auto a) {
             now.template write<decltype(a)::value, E::kGated>(p.e, static_cast<O*>(p.C), p.ldc, ep, kPitch, row0 + 16 * i, col0,
-                                                              left(i), cols, zero);
+                                                              left(i), cols, false);
         });
         __builtin_amdgcn_s_waitcnt(0xC07F);                     // reads done before the next rows' writes
         __builtin_amdgcn_wave_barrier();
@@ -656,9 +734,21 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
     char* C = static_cast<char*>(p.C);
     bool zero = false;
     int32_t grp = 0;
+    // with an epilogue 256-row tiles may have 128 rows: the waves of the others load and multiply nothing
+    constexpr bool kPairs = E::kOn && P::kTM == 256;
+    static_assert(!kPairs || P::kStages == 2, "waves' loads may differ in number: all are waited for");
+    uint32_t pair_rows = 256u;
     if (p.mode == 0) {
-        if (p.offs != nullptr) {
-            // Row groups (launched with 128-row tiles only: one group unit).
+        if (kPairs && p.offs != nullptr) {
+            const uint32_t j = blockIdx.x >> 3;
+            if (!pair_tile(p, blockIdx.x & 7u, j / p.tiles_n, &m0, &pair_rows, &grp)) return;   // uniform
+            tn = j % p.tiles_n;
+            zero = grp >= p.G;
+            if (zero) grp = 0;
+            B += int64_t(grp) * p.b_gs;
+            sB += int64_t(grp) * p.sb_gs;
+        } else if (p.offs != nullptr) {
+            // Row groups in 128-row tiles: one group unit.
             // Workgroups are dealt to the 8 XCDs in turn, each with its own
             // L2.  XCD x (workgroups x, x + 8, ...) takes a contiguous range of the
             // covered row tiles, every column tile of one row tile in a row,
@@ -703,6 +793,20 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
     }
     constexpr int kCols = E::kGated ? P::kTN / 2 : P::kTN;      // results of a tile's row
     const int64_t n0 = int64_t(tn) * kCols;
+    if constexpr (E::kOn) {
+        if (zero) {                                             // uniform: the tail
+            using O = std::conditional_t<kOut == 0, float, __bf16>;
+            const uint32_t rows = min(kPairs ? pair_rows : uint32_t(P::kTM), uint32_t(min(int64_t(P::kTM), p.M - m0)));
+            const uint32_t cols = uint32_t(min(int64_t(kCols), p.N - n0));
+            clear_rows<O, P::kThreads>(static_cast<O*>(p.C) + m0 * p.ldc + n0, p.ldc, rows, cols);
+            if (p.e.pre) {
+                O* pre = static_cast<O*>(p.e.pre) + m0 * p.e.ld_pre + n0;
+                clear_rows<O, P::kThreads>(pre, p.e.ld_pre, rows, cols);
+                if (E::kGated) clear_rows<O, P::kThreads>(pre + p.e.up, p.e.ld_pre, rows, cols);
+            }
+            return;
+        }
+    }
     const int64_t n = zero ? 0 : (k_hi - k_lo) / kTile;
 
     // ---- load plan (all offsets fit 32 bits: a tile spans <= 256 rows of <= 2^24 bytes) ----
@@ -710,7 +814,8 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
     const uint32_t lr = lane >> 3, lc = (lane & 7u) ^ (lane >> 3);
     const uint32_t voa = lr * lda + 16u * lc, vob = lr * ldb + 16u * lc;
     // M and N are multiples of 128: rows past a ragged last tile wrap onto valid rows
-    const uint32_t a_mask = uint32_t(min(int64_t(P::kTM), p.M - m0)) - 1u;
+    const uint32_t m_rows = min(kPairs ? pair_rows : uint32_t(P::kTM), uint32_t(min(int64_t(P::kTM), p.M - m0)));
+    const uint32_t a_mask = m_rows - 1u;
     const uint32_t b_mask = uint32_t(min(int64_t(P::kTN), p.N - n0)) - 1u;
     const v4i ra = pipe_rsrc(p.A + m0 * p.lda);
     // gated: N is whole tiles, and all of a wave's rows of B are of one half
@@ -759,6 +864,7 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
         const uint32_t st_ = lds0 + uint32_t((step) % P::kStages) * kStageB;                     \
         _Pragma("unroll") for (int q_ = 0; q_ < P::kLA; ++q_) {                                  \
             const uint32_t j_ = uint32_t(P::kLA) * wave + q_;                                    \
+            if (kPairs && 8u * j_ >= m_rows) continue;                                           \
             pipe_load16(ra, st_ + P::kA + 1024u * j_, voa, ((8u * j_) & a_mask) * lda + k_);     \
         }                                                                                        \
         _Pragma("unroll") for (int q_ = 0; q_ < P::kLB; ++q_) {                                  \
@@ -798,6 +904,18 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
             if constexpr (kPer)
                 if (s0 == 0) MXQ_PERIOD_ISSUE(0);
             MXQ_PIPE_ISSUE(s0);
+        }
+    }
+    if constexpr (kPairs) {
+        if (wm * (16u * MS) >= m_rows) {                        // uniform for the wave: no rows, its part of B's loads
+            for (int64_t s = 0; s < n; ++s) {
+                pipe_sync<0>();
+                if constexpr (kPer)
+                    if (s % 4 == 0 && 4 * (s / 4 + 1) < n) MXQ_PERIOD_ISSUE(s / 4 + 1);
+                if (s + 1 < n) MXQ_PIPE_ISSUE(s + 1);
+            }
+            __syncthreads();                                    // the epilogue's
+            return;
         }
     }
     for (int64_t s = 0; s < n; ++s) {
@@ -867,7 +985,7 @@ void mx_gemm_pipe_kernel(GemmArgs p) {
 #undef MXQ_PERIOD_ISSUE
     if constexpr (E::kOn) {
         using O = std::conditional_t<kOut == 0, float, __bf16>;
-        mx_store_act<O, MS, NS, E>(p, acc, lds, m0 + 16 * MS * wm, n0, wn, wave, grp, zero);
+        mx_store_act<O, MS, NS, E>(p, acc, lds, m0 + 16 * MS * wm, m0 + m_rows, n0, wn, wave, grp);
         return;
     }
     __syncthreads();
@@ -1078,8 +1196,10 @@ int plain_scale_form(const uint8_t* s, int64_t rs, int64_t bs, int64_t K, int64_
 }
 
 // Which tiles a product with an epilogue takes: the form that splits the
-// contraction, 128 x 256 or (dense only) 256 x 256, by the time that rounds of
-// them on 256 CUs take, fixed and for each step of the contraction.  Measured
+// contraction, 128 x 256 or 256 x 256, by the time that rounds of them on 256
+// CUs take, fixed and for each step of the contraction.  Row groups take 256
+// rows of one group from 192 rows a group on (pairs of units; half of the
+// groups are taken to leave one unit over), else 128.  Measured
 // (us for the three; dense, bf16 results, K = 5120 but where said):
 //   [128, 128] K 512       5.2   13.0   16.8    [1024, 2048] K 2048  17.4  25.0  37.4
 //   [128, 5120]           21.8   47.4   66.0    [1024, 5120]         95.6  51.1  71.4
@@ -1088,13 +1208,29 @@ int plain_scale_form(const uint8_t* s, int64_t rs, int64_t bs, int64_t K, int64_
 //   [512, 2048]           19.1   47.8   70.0    [2048, 5120]          201  96.1  73.6
 //   [512, 5120]           50.3   48.7   70.4    [4096, 2048] K 512   34.0  14.8  21.8
 //   [768, 5120]           70.2   49.9   71.5    [4096, 4096] K 4096   239  87.8  70.8
+// Row groups, gated, sums kept, 64 experts [2048, 5120] (us for 128 and 256
+// rows, and for 256 with B's loads past the caches; units a group, uneven but
+// where said):
+//   1, even    138   180   159        2, even    236   217   185
+//   1.5        191   212   179        2.5        336   302   278
+//   2          279   287   246        8.6       1047   855   900
+// and [2048, 1024], not gated, 2.5 units: 111, 90, 104: past the caches where
+// groups are shorter than four units and the experts' B do not fit the 256 MiB
+// of the last cache.
 enum class Tiles { kSplit, kHalf, kWhole };
+inline bool pair_units(const GemmArgs& p) { return p.M >= 192 * int64_t(p.G); }
+inline bool stream_pairs(const GemmArgs& p, int64_t W) {
+    return p.M < 512 * int64_t(p.G) && double(W) * double(p.K) * double(p.G) > double(1 << 28);
+}
 template <typename E>
 Tiles tile_form(const GemmArgs& p) {
     const int64_t W = E::kGated ? 2 * p.N : p.N, steps = p.K / kTile;
     auto time = [&](int64_t tiles, double fixed, double step) { return double((tiles + 255) / 256) * (fixed + step * double(steps)); };
-    const double split = time(p.M / 64 * (W / 64), 3.0, 0.40), half = time(p.M / 128 * ((W + 255) / 256), 9.0, 0.95);
-    const double whole = p.offs ? 1e30 : time((p.M + 255) / 256 * ((W + 255) / 256), 11.0, 1.45);
+    const bool groups = p.offs != nullptr, pairs = groups && pair_units(p);
+    const int64_t rows = groups ? (p.M / 128 + p.G / 2 + 1) / 2 : (p.M + 255) / 256, cols = (W + 255) / 256;
+    const double split = time(p.M / 64 * (W / 64), 3.0, 0.40);
+    const double half = pairs ? 1e30 : time(p.M / 128 * cols, 9.0, 0.95);
+    const double whole = groups && !pairs ? 1e30 : time(rows * cols, 11.0, 1.45);
     return split <= half && split <= whole ? Tiles::kSplit : half <= whole ? Tiles::kHalf : Tiles::kWhole;
 }
 
@@ -1111,11 +1247,31 @@ hipError_t launch_half(GemmArgs& p, int out_dtype, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Row groups with an epilogue in 256 x 256 tiles of up to two units of a group:
+// at most half the units, half the groups (an odd unit each) and the tail's.
+template <int kSF, bool kStreamB, typename E>
+hipError_t launch_pairs(GemmArgs& p, int out_dtype, hipStream_t stream) {
+    using P = Pipe<4, 8, 4, 2>;
+    constexpr int kCols = E::kGated ? P::kTN / 2 : P::kTN;
+    const int64_t units = p.M / 128, tiles = (units + (p.G < units ? p.G : units) + 1) / 2;
+    p.tiles_n = uint32_t((p.N + kCols - 1) / kCols);
+    // an XCD's ranges of the groups' tiles and of the tail's are a ceiling each
+    const dim3 grid(8u * uint32_t((tiles + 7) / 8 + 1) * p.tiles_n), block(P::kThreads);
+    if (out_dtype == 0) hipLaunchKernelGGL((mx_gemm_pipe_kernel<0, 4, 8, 4, 2, kSF, kStreamB, E>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((mx_gemm_pipe_kernel<1, 4, 8, 4, 2, kSF, kStreamB, E>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
 // Row groups: 128-row tiles (one group unit) of 8 waves; otherwise 256 x 256.
 template <int kSF, typename E>
 hipError_t launch_pipe(GemmArgs& p, int out_dtype, hipStream_t stream) {
     if constexpr (E::kOn) {                                     // others keep the order of their sums
         if (p.offs == nullptr && tile_form<E>(p) == Tiles::kHalf) return launch_half<kSF, E>(p, out_dtype, stream);
+    }
+    if constexpr (E::kOn) {
+        if (p.offs != nullptr && pair_units(p))
+            return stream_pairs(p, E::kGated ? 2 * p.N : p.N) ? launch_pairs<kSF, true, E>(p, out_dtype, stream)
+                                                              : launch_pairs<kSF, false, E>(p, out_dtype, stream);
     }
     if (p.mode == 0 && p.offs != nullptr) {
         // 128 x 256 tiles (a group unit is 128 rows).  Each XCD's share is at

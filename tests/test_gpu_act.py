@@ -281,7 +281,9 @@ def test_mx_dense(M, N, K, out, gated):
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("sizes,tail,N,K", [([128, 0, 256, 128], 128, 256, 512), ([0, 0, 384], 0, 128, 256),
                                             ([128] * 5 + [640], 256, 384, 1152),
-                                            ([1280, 0, 128, 768], 640, 2048, 256), ([128, 256] * 8, 128, 1024, 384)])
+                                            ([1280, 0, 128, 768], 640, 2048, 256), ([128, 256] * 8, 128, 1024, 384),
+                                            ([128] * 20 + [0] * 4, 128, 2048, 256), ([0, 384] * 35 + [256], 384, 640, 256),
+                                            ([640, 0, 1152, 128], 128, 3200, 128)])
 def test_mx_by_expert(sizes, tail, N, K, out, gated, form):
     g = gen(sum(sizes) + N)
     M, G, W = sum(sizes) + tail, len(sizes), 2 * N if gated else N
@@ -326,6 +328,36 @@ def test_a_bias_that_experts_share_and_experts_without_rows(gated):
         assert torch.equal(call(one.expand(E, W)), want)
         assert torch.equal(call(wide[:, :W]), want)
         assert torch.equal(call(one.repeat(G, 1)), want)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_mx_by_many_experts(gated, form):
+    """70 experts whose B exceed the last cache, and 23 of them at a time: the
+    same rows give the same bits."""
+    g = gen(69 + gated)
+    G, W, K = 70, 2048, 2048
+    N = W // 2 if gated else W
+    sizes = np.array([0, 128, 256, 384, 512, 128, 384] * 10)
+    ends = np.cumsum(sizes)
+    M = int(ends[-1]) + 256
+    A = Operand((M, K), g, K)
+    B = Operand((G, W, K), g, K)
+    B.v = None
+    bias = torch.randn((G, W), generator=g, device=DEV)
+    call = mxq.mx_grouped_gemm_rows_act_mfma if form == "mfma" else mxq.mx_grouped_gemm_rows_act
+    sA, sB = A.scales(form), B.scales(form)
+    offs = torch.from_numpy(ends.astype(np.int32)).to(DEV)
+    y, pre = call(A.q, sA, B.q, sB, offs, bias, "gelu", gated, pre=True)
+    assert not y[ends[-1]:].any() and not pre[ends[-1]:].any()
+    for e0 in range(0, G, 23):
+        e1 = min(e0 + 23, G)
+        r0, r1 = int(ends[e0] - sizes[e0]), int(ends[e1 - 1])
+        rows = A.s[r0:r1]
+        part = {"rows": lambda s: s, "odd": lambda s: s.repeat_interleave(3, dim=-1)[..., ::3],
+                "blocks": lambda s: s.transpose(-1, -2).contiguous().transpose(-1, -2), "mfma": mxq.scales_to_mfma}[form](rows)
+        ye, pe = call(A.q[r0:r1], part, B.q[e0:e1], sB[e0:e1], offs[e0:e1] - r0, bias[e0:e1], "gelu", gated, pre=True)
+        assert torch.equal(y[r0:r1], ye) and torch.equal(pre[r0:r1], pe), e0
 
 
 def test_mx_without_a_contraction_is_refused():
