@@ -360,6 +360,42 @@ def test_mx_by_many_experts(gated, form):
         assert torch.equal(y[r0:r1], ye) and torch.equal(pre[r0:r1], pe), e0
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("sizes,tail,N,K", [([640, 0, 1152, 128], 384, 3200, 128), ([128] * 20 + [0] * 4, 256, 2048, 256),
+                                            ([128, 0, 256], 128, 128, 256)])
+def test_mx_by_expert_into_any_rows(sizes, tail, N, K, gated, out):
+    """Results and kept sums at any element and pitch: the bits of contiguous
+    ones, the tail 0, what surrounds them as it was."""
+    g = gen(sum(sizes) + K)
+    M, G, W = sum(sizes) + tail, len(sizes), 2 * N if gated else N
+    A, B = Operand((M, K), g, K), Operand((G, W, K), g, K)
+    bias = torch.randn((G, W), generator=g, device=DEV)
+    offs = torch.from_numpy(np.cumsum(sizes).astype(np.int32)).to(DEV)
+    ops = (A.q, A.s, B.q, B.s, offs, bias, "gelu_tanh", gated)
+    want, kept = mxq.mx_grouped_gemm_rows_act(*ops, out_dtype=DT[out], pre=True)
+    assert not want[M - tail:].any() and not kept[M - tail:].any() and want[:M - tail].any(1).all()
+    y, pre = (torch.full((M, n + 5), 9.0, dtype=DT[out], device=DEV) for n in (N, W))
+    mxq.mx_grouped_gemm_rows_act(*ops, out=y[:, 3:N + 3], pre=pre[:, 1:W + 1])
+    assert torch.equal(y[:, 3:N + 3], want) and torch.equal(pre[:, 1:W + 1], kept)
+    assert (y[:, :3] == 9).all() and (y[:, N + 3:] == 9).all() and (pre[:, :1] == 9).all() and (pre[:, W + 1:] == 9).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(2304, 3200, 128), (1280, 3200, 256), (384, 128, 256)])
+def test_mx_ends_that_are_none(M, N, K):
+    """Ends below 0, past the rows, descending or inside a unit: as the ends
+    rounded down to units and clamped to an ascending sequence."""
+    g = gen(M)
+    bad = np.array([-300, 300, 130, 10 ** 9, 700, -2 ** 31, M + 1, 2 ** 31 - 1])[[0, 1, 2, 4, 5, 3, 6, 7]]
+    good = np.maximum.accumulate(np.clip(bad, 0, M) // 128 * 128)
+    A, B = Operand((M, K), g, K), Operand((8, N, K), g, K)
+    call = lambda e: mxq.mx_grouped_gemm_rows_act(A.q, A.s, B.q, B.s, torch.from_numpy(e.astype(np.int32)).to(DEV), act="silu",  # noqa: E731
+                                                  pre=True)
+    for n in (5, 8):                                           # with a tail, and the rest to one group
+        for a, b in zip(call(bad[:n]), call(good[:n])):
+            assert torch.equal(a, b)
+
+
 def test_mx_without_a_contraction_is_refused():
     """As mx_gemm_nt's: torch's empty operands have no address."""
     q, s = torch.empty((128, 0), dtype=torch.uint8, device=DEV), torch.empty((128, 0), dtype=torch.uint8, device=DEV)
