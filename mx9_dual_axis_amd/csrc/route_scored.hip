@@ -31,11 +31,12 @@
 // in binary64 from the logits in LDS, pick by pick.
 //
 // Bound by vector instructions: 131072 x 256 fp32 by sigmoid scores, a bias and
-// 8 groups take 117 us (the call 128; without groups 101).  A round of four
-// tokens is 1428 instructions; they fill half of the cycles.  Tokens are decided
+// 8 groups take 115 us (the call 122; without groups 95).  Scores that picks go
+// by are formed briefly (act.h), weights are not: 6 us less.  A round of four
+// tokens was 1428 instructions before; they filled half of the cycles.  Tokens are decided
 // again after the pass, so that what they need takes no registers from the
 // others (within it the call took 301 us).  They are few, about one in 1500 here,
-// but a block waits some 10 us for one: without that code the call takes 105 us.
+// but a block waits some 10 us for one: without that code the call took 105 us instead of 128.
 #include "act.h"
 #include "route_device.h"
 
@@ -308,7 +309,7 @@ __device__ __forceinline__ uint32_t groups_exactly(const RouteArgs& p, const Sco
             one = fmaxf(one, w);
         }
         const float low = a.best == 2 && two > -INFINITY ? two : one;
-        const float from = low - (a.bias ? r.near : (a.softmax ? 0x1p-15f : 0x1p-19f) * low);
+        const float from = low - (a.bias ? r.near : 0x1p-15f * low);
         int32_t n = 0, c0 = 0, c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll 1
         for (int32_t e = e0; e < e1; ++e) {
@@ -476,8 +477,7 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
             float sum = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float q;
-                u[v] = sc.softmax ? __expf(z[v] - sc.top) : act_logistic(z[v], &q);
+                u[v] = sc.softmax ? __expf(z[v] - sc.top) : act_logistic_brief(z[v]);
                 sum += u[v];
             }
             sum = row_sum(sum);
@@ -486,9 +486,9 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] = __fmaf_rn(u[v], inv, acc[v]);
             if (l16 == 0 && some) atomicAdd(&sh_live, 1);
-            // How far a score may be from its binary64 value.  Sigmoid: e^-|z| within
-            // 1.6 2^-23 of itself, which moves s by a quarter of that at most, the sum and
-            // the reciprocal 1.5 2^-23: 2^-22 in all.  Softmax: p |d| 2^-23 <= 2^-24, and
+            // How far a score may be from its binary64 value.  Sigmoid: e^-z within
+            // 1.25 |z| 2^-24 + 2^-23 of itself, which moves s by s (1 - s) of that, 0.4 2^-23
+            // at most, the sum and the reciprocal 1.5 2^-23: 2^-22 in all.  Softmax: p |d| 2^-23 <= 2^-24, and
             // 2^-24 p for each of V + 4 additions and the mean |d| <= ln E of the sum.
             const float off = sc.softmax ? 0x1p-24f * (1.f + float(V + 24) * inv) : 0x1p-22f;
             // what groups are weighed by: u with a bias, else s
@@ -605,9 +605,9 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
                 mag = row_max(mag);
                 largest = mag;
                 // two scores to a worth, two worths to a comparison; without a bias
-                // scores are as close as their own size says: a sigmoid one within
-                // 2^-21 of it, a softmax one (|d| <= 87 below the largest) 2^-16
-                const float near = biased ? 4.f * off + 0x1p-21f * mag : (sc.softmax ? 0x1p-15f : 0x1p-19f) * inside;
+                // scores are as close as their own size says: within 2^-16 of it (a
+                // softmax one |d| <= 87 below the largest, a sigmoid one |z| <= 88)
+                const float near = biased ? 4.f * off + 0x1p-21f * mag : 0x1p-15f * inside;
                 unsure = outside > -INFINITY && !(inside - outside > near);
                 auto kept = [&](int v) { return ((stays >> (uint32_t(S::expert(l16, v)) * a.inverse >> 20)) & 1u) != 0; };
                 if (a.size % S::kC == 0) {                                  // a lane's pieces lie in one group each
