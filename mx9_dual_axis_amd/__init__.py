@@ -23,8 +23,8 @@ when ``offs`` is None, grouped otherwise), ``convert_to_mx9`` and
 ``convert_to_mx9_packed`` / ``convert_from_mx9_packed``.
 
 ``routed`` holds what stands between the tokens of a routed-expert layer and
-these calls (routing with its balance loss, dispatch, combine, their
-gradients) and the product of 8-bit integer codes; ``act`` the products of both
+these calls (routing by softmax or by balanced scores with its balance loss,
+dispatch, combine, their gradients) and the product of 8-bit integer codes; ``act`` the products of both
 kinds with bias, activation and residual in their epilogue.  Their names are
 the package's too.
 """

@@ -249,7 +249,7 @@ FORMS = ("rows", "blocks", "mfma", "odd")
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 # Tiles of 64 x 64 whose waves split the contraction (the first four, with fewer
 # steps than waves and more), of 128 x 256, of 256 x 256, ragged ones among them.
-@pytest.mark.parametrize("M,N,K", [(128, 128, 128), (256, 384, 1024), (384, 640, 512), (640, 256, 1152), (2048, 1920, 256),
+@pytest.mark.parametrize("M,N,K", [(128, 128, 128), (1920, 5120, 256), (256, 384, 1024), (384, 640, 512), (640, 256, 1152), (2048, 1920, 256),
                                    (2048, 1152, 384), (4224, 3968, 128), (3968, 4224, 256)])
 def test_mx_dense(M, N, K, out, gated):
     g = gen(M + N + K)
