@@ -27,8 +27,9 @@
 // truly equal and in order by their keys.  Where one is found the experts that
 // come close enough to be picks (mostly one or two more than k) are ranked by
 // their binary64 values, a lane to each or two; where it is groups that are
-// close, or more than 32 experts, the four tokens of the wave are decided again
-// in binary64 from the logits in LDS, pick by pick.
+// close, or more than 32 experts, or the u span too little or too much for a
+// grid, the four tokens of the wave are decided again in binary64 from the
+// logits in LDS, pick by pick.
 //
 // Bound by vector instructions: 131072 x 256 fp32 by sigmoid scores, a bias and
 // 8 groups take 115 us (the call 122; without groups 95).  Scores that picks go
@@ -637,7 +638,10 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
             up = row_max(up);
             low = row_min(low);
             const float range = up - low;                                   // -inf where there is nothing
-            const float grid = range > 0.f && range < 1e30f ? 4194240.f / range : 0.f;
+            // no grid where a step of it, or its inverse, would leave fp32: everything is
+            // decided again
+            const bool gridless = range >= 1e30f || (up > low && range < 0x1p-100f);
+            const float grid = up > low && !gridless ? 4194240.f / range : 0.f;
             forget(u);
             // steps from 1 on; 0 of an expert that is none (no key below 1024 counts)
             auto key = [&](int v) {
@@ -705,14 +709,14 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
                 if (close != 0) close = apart;
             }
             close_picks = (row_or(close_picks) | uint32_t(close)) != 0;
-            if ((close_picks || unsure || range >= 1e30f) && !bad) {
+            if ((close_picks || unsure || gridless) && !bad) {
                 // decided again after the pass
                 if (l16 == 0) {
                     atomicOr(&again, 1ull << tok);
                     Again& r = redo[tok];
                     r.least = full ? xl - near - step : -INFINITY;
                     r.near = near + 0x1p-23f * largest;
-                    r.doubt = range >= 1e30f ? 2 : unsure ? 1 : 0;
+                    r.doubt = gridless ? 2 : unsure ? 1 : 0;
                     r.stays = staying;
                     r.top = sc.top;
                     r.inv = sc.inv;

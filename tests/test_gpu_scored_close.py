@@ -1,0 +1,67 @@
+"""GPU tests of scored routing where scores are close to each other, or too
+small for fp32: picks as binary64 decides them (scored_oracle, through the
+comparison that test_gpu_scored makes)."""
+import numpy as np
+import pytest
+import torch
+
+import mx9_dual_axis_amd as mxq
+import scored_oracle as so
+from helpers import require_gpu, say
+from test_gpu_scored import DEV, DT, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu(request):
+    require_gpu()
+    say(request.node.name)
+
+
+# What picks go by spans next to nothing: a step of the keys' grid is below
+# fp32's least normal number, or its inverse above the largest.
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("span", [1e-29, 1e-31, 2e-32, 1e-32, 1e-33, 1e-38, 1e-42])
+def test_logits_that_span_next_to_nothing(span, kind):
+    g = np.random.default_rng(29)
+    for row, k in (([0, 0, 1, 0], 3), ([0, 0, 1, 0], 1), ([0, 1], 2), ([1, 0], 2), ([0.25, 1, 0.5, 0.75], 2)):
+        z = torch.tensor(row, dtype=torch.float64).mul(span).float().repeat(5, 1).to(DEV)
+        check(z, k, kind)
+    for E, k in ((16, 4), (60, 8), (256, 8), (600, 16)):
+        for dtype in ("f32", "bf16"):
+            z = torch.from_numpy(g.random((70, E)) * span).to(DT[dtype])
+            z[3:, 1:E:7] = 0.0
+            z[5:, 2:E:5] = -torch.inf
+            z[7:40, E // 4:] = -torch.inf                                 # few experts
+            check(z.to(DEV), k, kind)
+            if E % 4 == 0:
+                check(z.to(DEV), k, kind, None, 4, 2, 2)
+
+
+@pytest.mark.parametrize("level", [-60.0, -73.0, -80.0, -83.0, -95.0])
+@pytest.mark.parametrize("E,k", [(2, 2), (4, 3), (16, 4), (256, 8)])
+def test_sigmoid_scores_next_to_nothing_with_a_bias(E, k, level):
+    """Biases of 0: u is the score itself.  (Below 2^-126 scores may be 0, which
+    shows in prob, whose sum has no more than 1e-20 added: picks alone there.)"""
+    g = np.random.default_rng(E)
+    z = np.float32(level + 0.5 * g.standard_normal((70, E)))
+    for bias in (np.zeros(E), np.where(np.arange(E) % 5 == 4, -np.inf, 0.0)):
+        for groups, top in ((1, 1), (4, 2)) if E >= 16 else ((1, 1),):
+            if level > -90:
+                check(torch.from_numpy(z).to(DEV), k, "sigmoid", bias, groups, top)
+                continue
+            r = mxq.mx_route_scored(torch.from_numpy(z).to(DEV), k, torch.from_numpy(bias).float().to(DEV), groups=groups,
+                                    top_groups=top, align=1)
+            want = so.route(z.astype(np.float64), k, "sigmoid", bias, groups, top, align=1, M=r.rows)
+            assert np.array_equal(r.idx.cpu().numpy(), want["idx"])
+
+
+@pytest.mark.parametrize("top", [60.0, 75.0, 86.0, 100.0])
+@pytest.mark.parametrize("E,k", [(3, 2), (16, 4), (256, 8)])
+def test_softmax_scores_next_to_nothing_with_a_bias(E, k, top):
+    """The largest score's expert is barred by its bias; the others' are e^-top of it."""
+    g = np.random.default_rng(E)
+    z = np.float32(g.standard_normal((70, E)))
+    z[:, 0] = top
+    check(torch.from_numpy(z).to(DEV), k, "softmax", np.where(np.arange(E) == 0, -np.inf, 0.0))
