@@ -261,6 +261,11 @@ __device__ int32_t rank_exactly(const ScoredArgs& a, int32_t E, int32_t k, const
     return int32_t(l16) < min(k, total) ? int32_t(list[l16]) : -1;
 }
 
+// How close to a worth w without a bias another tells nothing: scores are within
+// 2^-16 of their own size (a softmax one |d| <= 87 below the largest, a sigmoid
+// one |z| <= 88), and below 2^-126 they may be 0: two to each worth, 2^-124.
+__device__ __forceinline__ float close_worths(float w) { return 0x1p-15f * w + 0x1p-123f; }
+
 // What is kept of a token that is decided again.
 struct Again {
     float least;                 // experts of smaller u in those groups cannot be picks
@@ -310,7 +315,7 @@ __device__ __forceinline__ uint32_t groups_exactly(const RouteArgs& p, const Sco
             one = fmaxf(one, w);
         }
         const float low = a.best == 2 && two > -INFINITY ? two : one;
-        const float from = low - (a.bias ? r.near : 0x1p-15f * low);
+        const float from = low - (a.bias ? r.near : close_worths(low));
         int32_t n = 0, c0 = 0, c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll 1
         for (int32_t e = e0; e < e1; ++e) {
@@ -605,10 +610,8 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
                 outside = row_max(outside);
                 mag = row_max(mag);
                 largest = mag;
-                // two scores to a worth, two worths to a comparison; without a bias
-                // scores are as close as their own size says: within 2^-16 of it (a
-                // softmax one |d| <= 87 below the largest, a sigmoid one |z| <= 88)
-                const float near = biased ? 4.f * off + 0x1p-21f * mag : 0x1p-15f * inside;
+                // two scores to a worth, two worths to a comparison
+                const float near = biased ? 4.f * off + 0x1p-21f * mag : close_worths(inside);
                 unsure = outside > -INFINITY && !(inside - outside > near);
                 auto kept = [&](int v) { return ((stays >> (uint32_t(S::expert(l16, v)) * a.inverse >> 20)) & 1u) != 0; };
                 if (a.size % S::kC == 0) {                                  // a lane's pieces lie in one group each

@@ -65,3 +65,22 @@ def test_softmax_scores_next_to_nothing_with_a_bias(E, k, top):
     z = np.float32(g.standard_normal((70, E)))
     z[:, 0] = top
     check(torch.from_numpy(z).to(DEV), k, "softmax", np.where(np.arange(E) == 0, -np.inf, 0.0))
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("best", [1, 2])
+def test_worths_of_scores_that_fp32_loses(best, kind):
+    """Groups whose scores are about fp32's least normal number, some above and
+    some below it, without a bias: worths are sums of what binary64 has."""
+    g = np.random.default_rng(31)
+    high = 1.0 if kind == "sigmoid" else 0.0                          # (scores of 0.73, of a quarter)
+    z = np.full((300, 16), -120.0)
+    z[:, :4] = high
+    z[0, 4], z[0, 5], z[0, 8] = -87.0, -87.4, -86.9
+    z[1, 8], z[1, 9], z[1, 4] = -87.0, -87.4, -86.9
+    low = g.uniform(-89.5, -85.5, (298, 12))
+    z[2:, 4:] = np.where(g.random((298, 12)) < 0.6, low, z[2:, 4:])
+    z = np.float32(z)
+    for k, top in ((6, 2), (8, 3), (4, 2)):
+        check(torch.from_numpy(z).to(DEV), k, kind, None, 4, top, best)
+        check(torch.from_numpy(z).to(DEV), k, kind, None, 8, top + 1, best)
