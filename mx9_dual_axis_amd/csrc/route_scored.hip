@@ -385,7 +385,9 @@ __device__ __forceinline__ void decide_again(const RouteArgs& p, const ScoredArg
                     last = row_max(m);
                     at = int32_t(row_least(m == last ? uint32_t(me) : 0x7FFFFFFFu));
                 }
-                least = last > -INFINITY ? last - r.near : -INFINITY;
+                // (r.near knows the best u of these groups, not the k-th, whose
+                // rounding is 2^-24 of its own size, as the next one's)
+                least = last > -INFINITY ? last - r.near - (a.bias ? 0x1p-22f * fabsf(last) : 0.f) : -INFINITY;
             }
         }
     }

@@ -84,3 +84,19 @@ def test_worths_of_scores_that_fp32_loses(best, kind):
     for k, top in ((6, 2), (8, 3), (4, 2)):
         check(torch.from_numpy(z).to(DEV), k, kind, None, 4, top, best)
         check(torch.from_numpy(z).to(DEV), k, kind, None, 8, top + 1, best)
+
+
+def test_picks_of_a_group_that_is_found_again():
+    """Two groups whose worths only binary64 tells apart, the other one first; in
+    it two experts whose biases of some -1000 bring their sums within 2e-8 of the
+    same halfway point between fp32 numbers, which lie 6e-5 apart there."""
+    g = np.random.default_rng(37)
+    T, step = 3000, 2.0 ** -14
+    bias = np.array([0.0, -1, -1, -1, 0, -1000, -1000 - 6554 * step, -3000])
+    mid = (np.floor(g.uniform(0.15, 0.45, T) / step) + 0.5) * step
+    logit = lambda s: np.log(s / (1 - s))  # noqa: E731
+    z = g.standard_normal((T, 8))
+    z[:, 0], z[:, 4] = 0.0, 4e-9                                      # scores of 0.5 and 1e-9 more
+    z[:, 5], z[:, 6] = logit(mid), logit(mid + 6554 * step)
+    check(torch.from_numpy(z).float().to(DEV), 2, "sigmoid", bias, 2, 1, 1)
+    check(torch.from_numpy(z).float().to(DEV), 3, "sigmoid", bias, 2, 1, 1)
