@@ -31,13 +31,13 @@
 // grid, the four tokens of the wave are decided again in binary64 from the
 // logits in LDS, pick by pick.
 //
-// Bound by vector instructions: 131072 x 256 fp32 by sigmoid scores, a bias and
-// 8 groups take 115 us (the call 122; without groups 95).  Scores that picks go
-// by are formed briefly (act.h), weights are not: 6 us less.  A round of four
-// tokens was 1428 instructions before; they filled half of the cycles.  Tokens are decided
+// 131072 x 256 fp32 by sigmoid scores, a bias and 8 groups, with gradient and the
+// bias's step: 198 us (192 with scores formed in fewer operations, within 1.25
+// |z| 2^-24 of themselves: prob and loss are sums of them in fp32).  Vector
+// instructions fill about half of the first kernel's cycles.  Tokens are decided
 // again after the pass, so that what they need takes no registers from the
-// others (within it the call took 301 us).  They are few, about one in 1500 here,
-// but a block waits some 10 us for one: without that code the call took 105 us instead of 128.
+// others (within it the routing call took 301 us where it takes some 125).
+// They are few, about one in 1500 here, but a block waits some 10 us for one.
 #include "act.h"
 #include "route_device.h"
 
@@ -262,8 +262,8 @@ __device__ int32_t rank_exactly(const ScoredArgs& a, int32_t E, int32_t k, const
 }
 
 // How close to a worth w without a bias another tells nothing: scores are within
-// 2^-16 of their own size (a softmax one |d| <= 87 below the largest, a sigmoid
-// one |z| <= 88), and below 2^-126 they may be 0: two to each worth, 2^-124.
+// 2^-16 of their own size (a softmax one |d| <= 87 below the largest; a sigmoid
+// one within 2^-21), and below 2^-126 they may be 0: two to each worth, 2^-124.
 __device__ __forceinline__ float close_worths(float w) { return 0x1p-15f * w + 0x1p-123f; }
 
 // What is kept of a token that is decided again.
@@ -485,7 +485,8 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
             float sum = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                u[v] = sc.softmax ? __expf(z[v] - sc.top) : act_logistic_brief(z[v]);
+                float q;
+                u[v] = sc.softmax ? __expf(z[v] - sc.top) : act_logistic(z[v], &q);
                 sum += u[v];
             }
             sum = row_sum(sum);
@@ -494,9 +495,9 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] = __fmaf_rn(u[v], inv, acc[v]);
             if (l16 == 0 && some) atomicAdd(&sh_live, 1);
-            // How far a score may be from its binary64 value.  Sigmoid: e^-z within
-            // 1.25 |z| 2^-24 + 2^-23 of itself, which moves s by s (1 - s) of that, 0.4 2^-23
-            // at most, the sum and the reciprocal 1.5 2^-23: 2^-22 in all.  Softmax: p |d| 2^-23 <= 2^-24, and
+            // How far a score may be from its binary64 value.  Sigmoid: e^-|z| within
+            // 1.6 2^-23 of itself, which moves s by a quarter of that at most, the sum and
+            // the reciprocal 1.5 2^-23: 2^-22 in all.  Softmax: p |d| 2^-23 <= 2^-24, and
             // 2^-24 p for each of V + 4 additions and the mean |d| <= ln E of the sum.
             const float off = sc.softmax ? 0x1p-24f * (1.f + float(V + 24) * inv) : 0x1p-22f;
             // what groups are weighed by: u with a bias, else s

@@ -100,3 +100,18 @@ def test_picks_of_a_group_that_is_found_again():
     z[:, 5], z[:, 6] = logit(mid), logit(mid + 6554 * step)
     check(torch.from_numpy(z).float().to(DEV), 2, "sigmoid", bias, 2, 1, 1)
     check(torch.from_numpy(z).float().to(DEV), 3, "sigmoid", bias, 2, 1, 1)
+
+
+def test_shares_of_scores_far_from_zero():
+    """One token, one large score: the others' shares are their own scores.  A
+    score is within 16 u of itself whatever its logit (scored_oracle), so is the
+    sum; two additions of what is no more than 2^-60 of it, a reciprocal and a
+    product: 36 u."""
+    g = np.random.default_rng(41)
+    for E in (64, 256, 1000):
+        z = np.float32(g.uniform(-85, -60, (1, E)))
+        z[0, 3] = 20.0
+        s = so.scores(z[0].astype(np.float64), "sigmoid")
+        share = s / (s.sum() + so.EPS)
+        got = mxq.mx_route_scored(torch.from_numpy(z).to(DEV), 4, align=1).prob.double().cpu().numpy()
+        assert (np.abs(got - share) <= 36 * so.U * share).all(), (np.abs(got - share) / share / so.U).max()
