@@ -14,8 +14,9 @@
  *
  * act: MX_ACT_NONE x; MX_ACT_RELU max(x, 0); MX_ACT_SILU x / (1 + e^-x);
  * MX_ACT_GELU x Phi(x) with the normal distribution's Phi; MX_ACT_GELU_TANH
- * x / (1 + e^(-2 sqrt(2/pi) (x + 0.044715 x^3))).  A NaN gives NaN.  In fp32,
- * within some 2^-21 of the value; where y is bf16, within 2^-16.
+ * x / (1 + e^(-2 sqrt(2/pi) (x + 0.044715 x^3))).  A NaN gives NaN.  In fp32
+ * whatever y's type is (a bf16 y is the fp32 one, rounded), within some 2^-21 of
+ * the value.
  *
  * The conventions of mxq.h and mxq_routed.h hold.  bias f32 [W] or NULL; by
  * expert, group g's is bias + g * bias_gs.  residual [M, N] of the output's

@@ -9,11 +9,11 @@
 // rounding of its argument's product with log2 e, Phi is formed from erfc (1 +
 // erf loses its leading bits below 0), and 1 - p(x) is p(-x).  A NaN gives NaN.
 //
-// Values that a product rounds to bf16 (half steps of 2^-9) are formed in fewer
-// operations, kBrief: the argument's product with log2 e is not carried (some
-// 2^-23 |argument| of the result) and erfc's polynomial has degree 5 (2^-16).
-// A product's epilogue is bound by them where its contraction is short: each
-// of the two transcendental operations takes a wave 16 cycles, another one 4.
+// One formula whatever the results are rounded to: a bf16 result is the fp32 one,
+// rounded.  (Formed in fewer operations for bf16, within 2^-16 of the value,
+// 8192^3 took 513 us instead of 524 in MXFP8 with GELU, bias, residual and kept
+// sums, and 509 instead of 518 in int8 with tanh GELU; shorter products the same
+// within 0.3 us.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -70,34 +70,9 @@ __device__ __forceinline__ float act_tanh_arg(float x) {
     return 1.59576912f * __builtin_fmaf(0.044715f * x * x, x, x);
 }
 
-// p(x) and erfc(|x| / sqrt 2) / 2 as above, within what bf16 shows; the fit's
-// relative error is 1.2e-5.
-__device__ __forceinline__ float act_logistic_brief(float x) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269502f));
-}
-__device__ __forceinline__ float act_half_erfc_brief(float x) {
-    const float a = act_clamp(x, 20.f);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(a), 0.43f * 0.707106769f, 1.f));
-    float r = -0.0731139227f;
-    r = __builtin_fmaf(r, t, 0.193060535f);
-    r = __builtin_fmaf(r, t, 0.00615250011f);
-    r = __builtin_fmaf(r, t, 0.134722842f);
-    r = __builtin_fmaf(r, t, 0.11768082f);
-    r = __builtin_fmaf(r, t, 0.121503305f);
-    return r * t * __builtin_amdgcn_exp2f(a * a * (-0.5f * 1.44269502f));
-}
-
-template <int kAct, bool kBrief>
+template <int kAct>
 __device__ __forceinline__ float act_value(float x) {
     if constexpr (kAct == kActRelu) return x < 0.f ? 0.f : x;
-    if constexpr (kBrief) {
-        if constexpr (kAct == kActSilu) return x * act_logistic_brief(x);
-        if constexpr (kAct == kActGeluTanh) return x * act_logistic_brief(act_tanh_arg(x));
-        if constexpr (kAct == kActGelu) {
-            const float r = act_half_erfc_brief(x);
-            return x * (x < 0.f ? r : 1.f - r);
-        }
-    }
     float q;
     if constexpr (kAct == kActSilu) return x * act_logistic(x, &q);
     if constexpr (kAct == kActGelu) {

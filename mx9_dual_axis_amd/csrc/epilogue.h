@@ -112,7 +112,7 @@ struct EpRows {
             __builtin_memcpy(r, &res[q], 16);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                float v = act_value<kAct, sizeof(O) == 2>(x[i]);
+                float v = act_value<kAct>(x[i]);
                 if (kGated) v *= u[i];
                 if (e.residual) v += float(r[i]);
                 y[i] = ep_round<O>(zero ? 0.f : v);
@@ -156,7 +156,7 @@ __device__ __forceinline__ void each_index(int i, F&& f) {
 template <typename O, bool kGated>
 __device__ __forceinline__ O ep_one(const Epilogue& e, float x, float u, float residual) {
     float v = x;
-    act_switch(e.act, [&](auto a) { v = act_value<decltype(a)::value, sizeof(O) == 2>(x); });
+    act_switch(e.act, [&](auto a) { v = act_value<decltype(a)::value>(x); });
     if (kGated) v *= u;
     if (e.residual) v += residual;
     return ep_round<O>(v);
