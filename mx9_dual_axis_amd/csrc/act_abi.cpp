@@ -102,10 +102,11 @@ int mx_call(const uint8_t* A, int64_t lda, const uint8_t* sA, int64_t sa_rs, int
             bool mfma, void* stream) {
     if (N < 0 || N > kMaxGemm) return MX_E_SHAPE;
     const int64_t W = x.gated ? 2 * N : N;
-    // The products' own checks, of W channels: C's pitch counts beyond its N
-    // results, and an N that is not whole tiles is refused as such a W.
+    // The products' own checks, of W channels: a pitch of C that holds its N results
+    // stands for one that holds W, and an N that is not whole tiles is refused as
+    // such a W.
     int rc = check_gemm(A, lda, sA, sa_rs, sa_bs, B, ldb, sB, sb_rs, sb_bs, M, N % 128 == 0 ? W : 1, K, C,
-                        ldc < N || ldc > kMaxGemm ? -1 : ldc + (W - N), out_dtype, mfma);
+                        ldc < N ? -1 : ldc < W ? W : ldc, out_dtype, mfma);
     if (rc != MX_OK) return rc;
     if (groups && (G < 1 || G > (1 << 20))) return MX_E_SHAPE;
     if (!gemm_grid_fits(M, W, G, groups, false)) return MX_E_SHAPE;     // (smaller tiles are taken where they are few)
