@@ -42,6 +42,14 @@ template <typename O> __device__ __forceinline__ O ep_round(float x);
 template <> __device__ __forceinline__ float ep_round<float>(float x) { return x; }
 template <> __device__ __forceinline__ __bf16 ep_round<__bf16>(float x) { return __bf16(x); }   // nearest-even
 
+// An addition by itself: fused with the product before it where the two meet in
+// the code, and rounded twice elsewhere, a row's bits would go by the form that
+// its batch takes.
+__device__ __forceinline__ float ep_add(float x, float y) {
+#pragma clang fp contract(off)
+    return x + y;
+}
+
 // kCols columns (results) of 16 rows of one wave.
 template <typename O, int kCols>
 struct EpRows {
@@ -114,7 +122,7 @@ struct EpRows {
             for (int i = 0; i < kPer; ++i) {
                 float v = act_value<kAct>(x[i]);
                 if (kGated) v *= u[i];
-                if (e.residual) v += float(r[i]);
+                if (e.residual) v = ep_add(v, float(r[i]));
                 y[i] = ep_round<O>(zero ? 0.f : v);
                 g[i] = ep_round<O>(zero ? 0.f : x[i]);
                 if (kGated) h[i] = ep_round<O>(zero ? 0.f : u[i]);
@@ -158,7 +166,7 @@ __device__ __forceinline__ O ep_one(const Epilogue& e, float x, float u, float r
     float v = x;
     act_switch(e.act, [&](auto a) { v = act_value<decltype(a)::value>(x); });
     if (kGated) v *= u;
-    if (e.residual) v += residual;
+    if (e.residual) v = ep_add(v, residual);
     return ep_round<O>(v);
 }
 

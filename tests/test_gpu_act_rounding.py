@@ -102,3 +102,21 @@ def test_by_expert_rounds_the_fp32_result(sizes, N, K, act, gated):
     b, sb = codes((G, W, K), g), small_scales(G * W, 1, g).view(G, W)
     ops = (a, sa, b, sb, offs, bias, act, gated)
     assert torch.equal(mxq.i8_grouped_gemm_rows_act(*ops), mxq.i8_grouped_gemm_rows_act(*ops, out_dtype=torch.float32).bfloat16())
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [512, 333])
+def test_i8_rows_do_not_depend_on_their_batch(K, dtype, gated, biased):
+    """With a residual, through forms that add it in different places."""
+    g = gen(K + 57)
+    M, N = 3000, 333
+    W = 2 * N if gated else N
+    x, b, sb = torch.randn((M, K), generator=g, device=DEV).to(dtype), codes((W, K), g), small_scales(W, K, g)
+    bias = torch.randn(W, generator=g, device=DEV) if biased else None
+    res = torch.randn((M, N), generator=g, device=DEV).to(dtype)
+    for act in ao.ACTS:
+        whole = mxq.i8_linear_act(x, b, sb, bias, act, gated, res)
+        for m in (1, 16, 17, 65, 300):
+            assert torch.equal(mxq.i8_linear_act(x[:m], b, sb, bias, act, gated, res[:m]), whole[:m]), (act, m)
