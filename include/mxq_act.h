@@ -15,8 +15,10 @@
  * act: MX_ACT_NONE x; MX_ACT_RELU max(x, 0); MX_ACT_SILU x / (1 + e^-x);
  * MX_ACT_GELU x Phi(x) with the normal distribution's Phi; MX_ACT_GELU_TANH
  * x / (1 + e^(-2 sqrt(2/pi) (x + 0.044715 x^3))).  A NaN gives NaN.  In fp32
- * whatever y's type is (a bf16 y is the fp32 one, rounded), within some 2^-21 of
- * the value.
+ * whatever y's type is (a bf16 y is the fp32 one, rounded): SILU and GELU within
+ * 2^-20 of the value; GELU_TANH, whose argument t = 2 sqrt(2/pi) (x + 0.044715
+ * x^3) is rounded on the way, within 2^-20 + 4 |t| 2^-24; values below 2^-118 may
+ * be 0.
  *
  * The conventions of mxq.h and mxq_routed.h hold.  bias f32 [W] or NULL; by
  * expert, group g's is bias + g * bias_gs.  residual [M, N] of the output's
@@ -64,7 +66,12 @@ int i8_grouped_gemm_rows_act(const int8_t *A, int64_t lda, const float *sA, cons
 /*
  * mx_gemm_nt_act, mx_grouped_gemm_rows_act -- mx_gemm_nt and
  * mx_grouped_gemm_rows with the epilogue: B [W, K], sB its scales; N a multiple
- * of 128.  The tail (rows from offs[G-1] on) gives 0 in C and in pre.  The
+ * of 128.  The sums are the matrix cores' and, as theirs, differ from exact ones
+ * by more than fp32's roundings.  Their order depends on M, W, K, the groups and
+ * the layout of the scales: the same call gives the same bits, but a row's bits,
+ * of y and of pre, may differ between calls of other sizes, and from
+ * mx_gemm_nt's.  (The 8-bit sums are exact: a row's bits there are its own.)
+ * The tail (rows from offs[G-1] on) gives 0 in C and in pre.  The
  * _mfma forms take both operands' scales in the matrix-core layout.  Errors as
  * of those calls, plus those above, MX_E_STRIDE for ld_pre below W and
  * MX_E_OVERLAP for pre with anything.  The pipelined kernel needs the scales
@@ -102,7 +109,8 @@ int mx_grouped_gemm_rows_act_mfma(const uint8_t *A, int64_t lda, const uint8_t *
  * offs[g] (dbias f32 [G, W]; groups of any size, empty ones give 0), in a
  * fixed order.  Rows from offs[G-1] on give 0 and are not read.  The
  * residual's gradient is dy.  act'(0) of MX_ACT_RELU is 0.  Infinite values of
- * pre have the slope's limit there.
+ * pre have the slope's limit there.  Slopes p + x p' (p what act(x) multiplies x
+ * by) are as accurate as the values, relative to |p| + |x p'|.
  *
  * workspace: mx_act_grad_workspace bytes, 4-byte aligned, where dbias is wanted
  * (-1 for arguments that mx_act_grad refuses).  Errors: MX_E_NULL, MX_E_DTYPE,

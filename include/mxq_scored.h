@@ -34,8 +34,10 @@ enum mx_score {
  *            (sigmoid) or s[e] (softmax)
  *
  * and slot, src, counts, offs, live, loss as mx_route's, loss with that prob.
- * u and worth are compared as the binary64 values of their formulas, so that
- * picks do not depend on how scores are rounded; everything else is fp32.
+ * u and worth are compared as the binary64 values of their formulas (formed
+ * within a few units of the last place), so that picks do not depend on how fp32
+ * rounds scores or loses small ones; everything else is fp32: a sigmoid score
+ * within 2^-20 of itself, a softmax one as mx_route's, those below 2^-126 may be 0.
  *
  * A logit of -inf bars the expert, and so does a bias that is not finite; a
  * token that is not valid, or has no logit above -inf, takes no part.  A valid

@@ -14,6 +14,11 @@ gates' channels and then as many more, y = act(x[:, :N]) * x[:, N:] (+
 residual).  act is "none", "relu", "silu", "gelu" or "gelu_tanh".  bias is
 float32 (a row for each expert in the grouped calls), residual has the
 result's shape and dtype and may be `out` itself.
+
+The 8-bit sums are exact, so a row's bits depend on that row alone.  The MXFP8
+sums are added in an order that depends on the call's sizes: the same call gives
+the same bits, but a row's may differ between batch sizes, and from those of
+mx_gemm_nt and mx_grouped_gemm_rows.
 """
 from __future__ import annotations
 

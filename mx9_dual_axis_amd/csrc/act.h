@@ -5,9 +5,14 @@
 //   gelu       x Phi(x),           Phi the normal distribution's integral
 //   gelu_tanh  x p(t),             t = 2 sqrt(2 / pi) (x + 0.044715 x^3)
 //
-// Errors stay within some 2^-21 of the result, in the tails too: e^x carries the
-// rounding of its argument's product with log2 e, Phi is formed from erfc (1 +
-// erf loses its leading bits below 0), and 1 - p(x) is p(-x).  A NaN gives NaN.
+// e^x carries the rounding of its argument's product with log2 e, Phi is formed
+// from erfc (1 + erf loses its leading bits below 0), and 1 - p(x) is p(-x), so
+// that tails keep their digits.  Largest errors measured over 2^20 points of each
+// of eleven ranges in [-80, 80], relative to the value: silu 2^-21.7, gelu
+// 2^-20.9; gelu_tanh 2^-21.5 for |x| <= 1 and 3.4 |t| 2^-24 beyond, since t is
+// rounded on the way (2^-18.6 at x = -5, 2^-16.3 at -10).  Slopes p + x p' have
+// the same errors, relative to |p| + |x p'|.  e^x ends at 2^-126: values below
+// 2^-118 may be 0.  A NaN gives NaN.
 //
 // One formula whatever the results are rounded to: a bf16 result is the fp32 one,
 // rounded.  (Formed in fewer operations for bf16, within 2^-16 of the value,

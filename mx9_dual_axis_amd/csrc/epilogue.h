@@ -13,12 +13,13 @@
 // pieces.  The residual of the 16 rows to come is read while these are
 // computed (but for 128 fp32 columns, where that would spill).
 //
-// What it adds to a product, 8192^3 MXFP8 to bf16 (us): the product alone 454;
-// with this epilogue and no activation 450, GELU 464, its bias 467, a residual
-// 482, the kept sums 490.  The tile's waves compute it while the matrix cores
-// wait (a tile's accumulators leave no room for a second tile on the CU), so an
-// activation costs its instructions: act.h.  The residual and the kept sums
-// cost their 134 MB each.
+// What it adds to a product, 8192^3 MXFP8 to bf16 (us, calls with a pause before
+// each; without pauses the clock is lower, 452 for the product alone): the
+// product alone 405; with this epilogue and no activation 425, SiLU 446, tanh GELU
+// 452, GELU 465, its bias 466, a residual 474, the kept sums 484.  The tile's waves
+// compute it while the matrix cores wait (a tile's accumulators leave no room for
+// a second tile on the CU), so an activation costs its instructions: act.h.  The
+// residual and the kept sums cost their 134 MB each.
 #pragma once
 
 #include "act.h"

@@ -272,6 +272,8 @@ void mx_gemm_kernel(GemmArgs p) {
     }
 
     // ---- epilogue: C[m0 + 64 wm + 16 ms + 4 (lane / 16) + v][n0 + 64 wn + 16 ns + lane % 16] ----
+    // (8192^3 with scales of neither layout, bf16: 1341 us alone; with GELU, bias,
+    // residual and kept sums, element by element, 1707)
     if constexpr (E::kOn) {
         using O = std::conditional_t<kOut == 0, float, __bf16>;
         constexpr int kN = E::kGated ? 2 : 4;                        // sub-tiles of results

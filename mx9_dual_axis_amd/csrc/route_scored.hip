@@ -31,13 +31,14 @@
 // grid, the four tokens of the wave are decided again in binary64 from the
 // logits in LDS, pick by pick.
 //
-// 131072 x 256 fp32 by sigmoid scores, a bias and 8 groups, with gradient and the
-// bias's step: 198 us (192 with scores formed in fewer operations, within 1.25
-// |z| 2^-24 of themselves: prob and loss are sums of them in fp32).  Vector
-// instructions fill about half of the first kernel's cycles.  Tokens are decided
-// again after the pass, so that what they need takes no registers from the
-// others (within it the routing call took 301 us where it takes some 125).
-// They are few, about one in 1500 here, but a block waits some 10 us for one.
+// 131072 x 256 fp32 by sigmoid scores, a bias and 8 groups: 128 us, without groups
+// 102 (the first kernel 119).  A round of four tokens is 1420 vector instructions,
+// which fill 49% of the first kernel's cycles.  The rest is mostly its end: tokens
+// are decided again after the pass, so that what they need takes no registers from
+// the others (within it the call took 301 us), and though they are few, about one
+// in 1500 here, a block waits some 10 us for one; by fp32 values alone the call
+// takes 97 us.  Scores formed in fewer operations (within 1.25 |z| 2^-24 of
+// themselves; prob and loss are sums of them in fp32): 122 us.
 #include "act.h"
 #include "route_device.h"
 
@@ -767,8 +768,8 @@ __global__ __launch_bounds__(kThr, kThr == 256 && V == 16 ? 4 : 1) void route_sc
 //   softmax: dlogits = s (a - sum a s) - s sum_j d_j s_j, + d_j s_j at idx_j
 //
 // One pass, as route.hip's gradient: a row is in registers between its scores
-// and the result.  131072 x 256 fp32: 62 us, 4.3 TB/s; the vector instructions
-// fill 62% of the cycles.
+// and the result.  131072 x 256 fp32: 62 us, 4.5 TB/s; the vector instructions
+// fill 64% of the cycles.
 struct ScoredGradArgs {
     const void* logits;
     int64_t ld;

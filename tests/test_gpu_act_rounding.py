@@ -1,5 +1,6 @@
 """GPU tests of bf16 results of products with an epilogue: they are the fp32
-formula's values, rounded once."""
+formula's values, rounded once.  (The wider bounds that act_oracle has for bf16,
+`brief`, are of a formula of fewer operations that results had before.)"""
 import pytest
 import torch
 

@@ -104,7 +104,8 @@ def test_picks_of_a_group_that_is_found_again():
 
 def test_shares_of_scores_far_from_zero():
     """One token, one large score: the others' shares are their own scores.  A
-    score is within 16 u of itself whatever its logit (scored_oracle), so is the
+    score is within 16 u of itself whatever its logit (scored_oracle; the wider
+    bound of test_gpu_scored's comparison is of scores whose argument was rounded), so is the
     sum; two additions of what is no more than 2^-60 of it, a reciprocal and a
     product: 36 u."""
     g = np.random.default_rng(41)
